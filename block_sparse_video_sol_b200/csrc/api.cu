@@ -398,6 +398,205 @@ sol_status sol_scatter_rows(const sol_params* p, const int32_t* perm, const void
   return rows_entry(p, perm, xp, x, false, stream, "sol_scatter_rows");
 }
 
+// ---- training: the attention's gradient, the norm with rotation -------------------------------
+namespace {
+
+struct BwdLayout {
+  int splits;
+  size_t nlse, ndelta, plan, tplan, gk, gv, gb, coef, da_part, da, total;
+};
+BwdLayout bwd_layout(const sol_params& p) {
+  BwdLayout R{};
+  const size_t bh = (size_t)p.B * p.H, nb = (p.N + kBlock - 1) / kBlock, tiles = bh * ((nb + 1) / 2);
+  const int mw = (int)((nb + 31) / 32);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
+  R.splits = attn_bwd_splits((int)nb);
+  R.nlse = take(bh * nb * kBlock * 4);
+  R.ndelta = take(bh * nb * kBlock * 4);
+  R.plan = take(tiles * plan_ints(mw, (int)nb) * 4);
+  R.tplan = take(tiles * tplan_ints((int)nb) * 4);
+  const size_t cent = p.routing == 1 ? 0 : 1, pooled = cent && p.log_mass_bias ? 1 : 0;
+  R.gk = take(cent * R.splits * bh * nb * p.D * 4);
+  R.gv = take(cent * R.splits * bh * nb * p.D * 4);
+  R.gb = take(cent * R.splits * bh * nb * 4);
+  R.coef = take(pooled * 3 * bh * nb * kBlock * 4);
+  R.da_part = take(pooled * bh * nb * p.D * 4);
+  R.da = take(pooled * bh * p.D * 4);
+  R.total = off;
+  return R;
+}
+
+// Output strides {b, n, h} (multiples of 8, each (b, n, h) a row of its own):
+// taken by size, every stride must clear what the smaller ones span.
+sol_status check_out_strides(const sol_params* p, const int64_t* st, const char* name) {
+  int64_t s[3] = {st[0], st[1], st[2]}, n[3] = {p->B, p->N, p->H};
+  for (int i = 0; i < 3; ++i)
+    if (s[i] < 0 || (s[i] & 7))
+      return fail(SOL_ERR_INVALID_ARG, "%s: output stride %lld must be >= 0 and a multiple of 8 elements", name, (long long)s[i]);
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (s[j] > s[j + 1]) { std::swap(s[j], s[j + 1]); std::swap(n[j], n[j + 1]); }
+  int64_t span = p->D;   // elements from a row's first to past the last of what the smaller strides reach
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (s[i] < span) return fail(SOL_ERR_INVALID_ARG, "%s: output strides make rows overlap", name);
+    span += s[i] * (n[i] - 1);
+  }
+  return SOL_OK;
+}
+
+sol_status check_norm_rope(const sol_params* p, const sol_norm_rope* nr, const char* name) {
+  if (!nr) return fail(SOL_ERR_INVALID_ARG, "%s: norm parameters are NULL", name);
+  if (nr->weight_type != 0 && nr->weight_type != 1) return fail(SOL_ERR_INVALID_ARG, "%s: weight_type must be 0 (fp32) or 1 (bf16)", name);
+  if (!(nr->eps >= 0.f) || isinf(nr->eps)) return fail(SOL_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", name);
+  if (nr->rot_dim < 0 || nr->rot_dim > p->D || (nr->rot_dim & 15))
+    return fail(SOL_ERR_INVALID_ARG, "%s: rot_dim %d must be a multiple of 16 in [0, %d]", name, nr->rot_dim, p->D);
+  if (nr->interleaved != 0 && nr->interleaved != 1) return fail(SOL_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1", name);
+  if (!aligned16(nr->q_weight) || !aligned16(nr->k_weight)) return fail(SOL_ERR_INVALID_ARG, "%s: weights not 16-byte aligned", name);
+  if (nr->rot_dim > 0) {
+    if (!nr->cos || !nr->sin) return fail(SOL_ERR_INVALID_ARG, "%s: NULL table", name);
+    if (!aligned16(nr->cos) || !aligned16(nr->sin)) return fail(SOL_ERR_INVALID_ARG, "%s: tables not 16-byte aligned", name);
+    if (nr->table_stride_b < 0 || nr->table_stride_n < 0 || (nr->table_stride_b & 3) || (nr->table_stride_n & 3))
+      return fail(SOL_ERR_INVALID_ARG, "%s: table strides must be >= 0 and multiples of 4 elements", name);
+  }
+  return SOL_OK;
+}
+
+NormRopeArgs norm_rope_args(const sol_params* p, const sol_norm_rope* nr, const void* q, const void* k) {
+  NormRopeArgs a{};
+  a.x[0] = static_cast<const __nv_bfloat16*>(q);
+  a.x[1] = static_cast<const __nv_bfloat16*>(k);
+  a.sb = p->in_stride_b; a.sn = p->in_stride_n; a.sh = p->in_stride_h;
+  a.ob = p->out_stride_b; a.on = p->out_stride_n; a.oh = p->out_stride_h;
+  a.w[0] = nr->q_weight; a.w[1] = nr->k_weight; a.w_bf16 = nr->weight_type;
+  a.eps = nr->eps;
+  a.half = nr->rot_dim / 2; a.inter = nr->interleaved;
+  a.cos = nr->cos; a.sin = nr->sin; a.tb = nr->table_stride_b; a.tn = nr->table_stride_n;
+  a.B = p->B; a.N = p->N; a.H = p->H;
+  return a;
+}
+
+}  // namespace
+
+size_t sol_attn_bwd_workspace_bytes(const sol_params* p) {
+  if (validate(p) != SOL_OK || empty(p) || p->qk_int8) return 0;
+  return bwd_layout(*p).total;
+}
+
+sol_status sol_attn_bwd(const sol_params* p, const void* q, const void* k, const void* v, const void* ws,
+                        size_t ws_bytes, const int32_t* row_ptr, const int32_t* col_idx, const void* o,
+                        const float* lse, const void* d_o, void* dq, void* dk, void* dv, const int64_t* g_strides,
+                        void* bws, size_t bws_bytes, void* stream) {
+  sol_status s = validate(p);
+  if (s != SOL_OK) return s;
+  if (p->qk_int8) return fail(SOL_ERR_UNSUPPORTED, "sol_attn_bwd: no gradient of INT8 QK (qk_int8 must be 0)");
+  if (empty(p)) return SOL_OK;
+  if (!q || !k || !v || !ws || !row_ptr || !col_idx || !o || !lse || !d_o || !dq || !dk || !dv || !bws)
+    return fail(SOL_ERR_INVALID_ARG, "sol_attn_bwd: NULL pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(d_o) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv))
+    return fail(SOL_ERR_INVALID_ARG, "sol_attn_bwd: tensors not 16-byte aligned");
+  const int64_t in_st[3] = {p->in_stride_b, p->in_stride_n, p->in_stride_h};
+  const int64_t* gs = g_strides ? g_strides : in_st;
+  if ((s = check_out_strides(p, gs, "sol_attn_bwd")) != SOL_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || (reinterpret_cast<uintptr_t>(bws) & 255u) != 0)
+    return fail(SOL_ERR_INVALID_ARG, "sol_attn_bwd: workspace not 256-byte aligned");
+  const WsLayout L = ws_layout(*p);
+  if (ws_bytes < L.total) return fail(SOL_ERR_WORKSPACE, "sol_attn_bwd: workspace %zu < %zu bytes", ws_bytes, L.total);
+  const BwdLayout R = bwd_layout(*p);
+  if (bws_bytes < R.total)
+    return fail(SOL_ERR_WORKSPACE, "sol_attn_bwd: backward workspace %zu < %zu bytes", bws_bytes, R.total);
+  int* status = nullptr;
+  if ((s = check_arch(&status)) != SOL_OK) return s;
+  BwdArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.sb = p->in_stride_b; a.sn = p->in_stride_n; a.sh = p->in_stride_h;
+  a.o = static_cast<const __nv_bfloat16*>(o);
+  a.d_o = static_cast<const __nv_bfloat16*>(d_o);
+  a.ob = p->out_stride_b; a.on = p->out_stride_n; a.oh = p->out_stride_h;
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  a.gb = gs[0]; a.gn = gs[1]; a.gh = gs[2];
+  a.lse = lse;
+  a.kbar16 = at<__nv_bfloat16>(ws, L.kbar16); a.vbar16 = at<__nv_bfloat16>(ws, L.vbar16);
+  a.cbias = at<float>(ws, L.cbias); a.anchor = at<float>(ws, L.anchor);
+  a.row_ptr = row_ptr; a.col_idx = col_idx;
+  a.B = p->B; a.N = p->N; a.H = p->H; a.nb = L.nqb; a.mask_words = L.mask_words;
+  a.prefix = p->prefix_len; a.mode = p->log_mass_bias; a.centroids = p->routing == 1 ? 0 : 1;
+  a.scale = eff_scale(p);
+  a.splits = R.splits;
+  a.nlse = at<float>(bws, R.nlse); a.ndelta = at<float>(bws, R.ndelta);
+  a.plan = at<int>(bws, R.plan); a.tplan = at<int>(bws, R.tplan);
+  a.gk = at<float>(bws, R.gk); a.gv = at<float>(bws, R.gv); a.gb_ = at<float>(bws, R.gb);
+  a.coef = at<float>(bws, R.coef); a.da_part = at<float>(bws, R.da_part);
+  a.da = a.centroids && a.mode ? at<float>(bws, R.da) : nullptr;
+  a.status = status;
+  const cudaError_t e = launch_attn_bwd(a, p->D, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "sol_attn_bwd launch");
+  return SOL_OK;
+}
+
+sol_status sol_qk_norm_rope(const sol_params* p, const sol_norm_rope* nr, const void* q, const void* k, void* qo,
+                            void* ko, void* stream) {
+  sol_status s = validate(p);
+  if (s != SOL_OK) return s;
+  if ((s = check_norm_rope(p, nr, "sol_qk_norm_rope")) != SOL_OK) return s;
+  if (empty(p)) return SOL_OK;
+  if (!q || !k || !qo || !ko) return fail(SOL_ERR_INVALID_ARG, "sol_qk_norm_rope: NULL pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(qo) || !aligned16(ko))
+    return fail(SOL_ERR_INVALID_ARG, "sol_qk_norm_rope: tensors not 16-byte aligned");
+  const int64_t out_st[3] = {p->out_stride_b, p->out_stride_n, p->out_stride_h};
+  if ((s = check_out_strides(p, out_st, "sol_qk_norm_rope")) != SOL_OK) return s;
+  if ((s = check_arch()) != SOL_OK) return s;
+  NormRopeArgs a = norm_rope_args(p, nr, q, k);
+  a.y[0] = static_cast<__nv_bfloat16*>(qo);
+  a.y[1] = static_cast<__nv_bfloat16*>(ko);
+  const cudaError_t e = launch_norm_rope(a, p->D, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "sol_qk_norm_rope launch");
+  return SOL_OK;
+}
+
+size_t sol_qk_norm_rope_bwd_workspace_bytes(const sol_params* p) {
+  if (validate(p) != SOL_OK || empty(p)) return 0;
+  return align256((size_t)2 * norm_rope_parts(p->B, p->N, p->H, p->D) * p->D * 4);
+}
+
+sol_status sol_qk_norm_rope_bwd(const sol_params* p, const sol_norm_rope* nr, const void* q, const void* k,
+                                const void* dqo, const void* dko, void* dq, void* dk, float* dq_weight,
+                                float* dk_weight, const int64_t* g_strides, void* ws, size_t ws_bytes, void* stream) {
+  sol_status s = validate(p);
+  if (s != SOL_OK) return s;
+  if ((s = check_norm_rope(p, nr, "sol_qk_norm_rope_bwd")) != SOL_OK) return s;
+  if (empty(p)) return SOL_OK;
+  if (!q || !k || !dqo || !dko || !dq || !dk || !ws) return fail(SOL_ERR_INVALID_ARG, "sol_qk_norm_rope_bwd: NULL pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(dqo) || !aligned16(dko) || !aligned16(dq) || !aligned16(dk) ||
+      !aligned16(dq_weight) || !aligned16(dk_weight))
+    return fail(SOL_ERR_INVALID_ARG, "sol_qk_norm_rope_bwd: tensors not 16-byte aligned");
+  const int64_t in_st[3] = {p->in_stride_b, p->in_stride_n, p->in_stride_h};
+  const int64_t* gs = g_strides ? g_strides : in_st;
+  if ((s = check_out_strides(p, gs, "sol_qk_norm_rope_bwd")) != SOL_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(SOL_ERR_INVALID_ARG, "sol_qk_norm_rope_bwd: workspace not 256-byte aligned");
+  const size_t need = sol_qk_norm_rope_bwd_workspace_bytes(p);
+  if (ws_bytes < need) return fail(SOL_ERR_WORKSPACE, "sol_qk_norm_rope_bwd: workspace %zu < %zu bytes", ws_bytes, need);
+  if ((s = check_arch()) != SOL_OK) return s;
+  NormRopeArgs a = norm_rope_args(p, nr, q, k);
+  a.dz[0] = static_cast<const __nv_bfloat16*>(dqo);
+  a.dz[1] = static_cast<const __nv_bfloat16*>(dko);
+  a.y[0] = static_cast<__nv_bfloat16*>(dq);
+  a.y[1] = static_cast<__nv_bfloat16*>(dk);
+  a.gb = gs[0]; a.gn = gs[1]; a.gh = gs[2];
+  a.dw[0] = dq_weight; a.dw[1] = dk_weight;
+  a.dw_part = static_cast<float*>(ws);
+  const cudaError_t e = launch_norm_rope_bwd(a, p->D, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "sol_qk_norm_rope_bwd launch");
+  return SOL_OK;
+}
+
 sol_status sol_debug_drop_arrive(int32_t step) {
 #ifdef SOL_FAULT_TEST
   sol_status s = check_arch();

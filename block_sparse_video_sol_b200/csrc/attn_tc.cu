@@ -981,9 +981,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   TcParams prm{a, (a.nkb + 31) / 32};
-  const int64_t tiles = (int64_t)a.B * a.H * ((a.nqb + 1) / 2);
-  plan_kernel<<<(unsigned)((tiles + kPlanWarps - 1) / kPlanWarps), kPlanWarps * 32, 0, st>>>(a, prm.mask_words);
-  cudaError_t pe = cudaGetLastError();
+  cudaError_t pe = launch_plan(a, st);
   if (pe != cudaSuccess) return pe;
   const size_t smem = 1024 + Cfg<D, I8>::kSmemTiles + sizeof(Extra<I8>);
   // Once per device (so that launches stay free of attribute calls, e.g.
@@ -1009,6 +1007,12 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_plan(const AttnArgs& a, cudaStream_t st) {
+  const int64_t tiles = (int64_t)a.B * a.H * ((a.nqb + 1) / 2);
+  plan_kernel<<<(unsigned)((tiles + kPlanWarps - 1) / kPlanWarps), kPlanWarps * 32, 0, st>>>(a, (a.nkb + 31) / 32);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_attn(const AttnArgs& a, int D, cudaStream_t st) {
   if (a.qk_int8) return D == 128 ? launch_tc<128, true>(a, st) : cudaErrorInvalidValue;

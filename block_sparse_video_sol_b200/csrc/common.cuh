@@ -158,8 +158,66 @@ size_t reblock_axis_floats(int BH, int n_v, int D);        // size of ReblockArg
 cudaError_t launch_reblock(const ReblockArgs& a, int iters, cudaStream_t st);
 cudaError_t launch_rows(const int32_t* perm, const __nv_bfloat16* src, __nv_bfloat16* dst, int B, int H, int N, int D,
                         int64_t sb, int64_t sn, int64_t sh, bool gather, int* status, cudaStream_t st);
+// The per-tile attention plans (plan_kernel) of a.row_ptr / a.col_idx into a.plan.
+cudaError_t launch_plan(const AttnArgs& a, cudaStream_t st);
 #ifdef SOL_FAULT_TEST
 cudaError_t set_drop_p_arrive(int step);   // fault-test build only
 #endif
+
+// ---- attention backward (sol_attn_bwd) ---------------------------------------------------------
+// Ints of one key tile's plan (two consecutive 64-row key blocks): a 16-int header
+// (list length), then the query blocks that take either of them exactly, ascending
+// (i | tile's first block << 16 | second block << 17).
+__host__ __device__ inline int tplan_ints(int nqb) { return (16 + nqb + 3) & ~3; }
+
+struct BwdArgs {
+  const __nv_bfloat16* q; const __nv_bfloat16* k; const __nv_bfloat16* v;
+  int64_t sb, sn, sh;            // strides of q, k, v
+  const __nv_bfloat16* o; const __nv_bfloat16* d_o;
+  int64_t ob, on, oh;            // strides of o, d_o
+  __nv_bfloat16* dq; __nv_bfloat16* dk; __nv_bfloat16* dv;
+  int64_t gb, gn, gh;            // strides of dq, dk, dv
+  const float* lse;
+  const __nv_bfloat16* kbar16; const __nv_bfloat16* vbar16; const float* cbias; const float* anchor;
+  const int32_t* row_ptr; const int32_t* col_idx;
+  int B, N, H, nb, mask_words;   // nb 64-row blocks of queries and of keys
+  int prefix, mode, centroids;   // mode: log_mass_bias
+  float scale;
+  int splits;                    // query ranges of the centroid pass
+  // caller-owned workspace
+  float* nlse;                   // [BH][64 nb]  -lse in log2 units, -inf for rows without keys or past N
+  float* ndelta;                 // [BH][64 nb]  -sum_d dO O, 0 past N
+  int* plan;                     // [BH * ceil(nb/2)][plan_ints]
+  int* tplan;                    // [BH * ceil(nb/2)][tplan_ints]
+  float* gk; float* gv;          // [splits][BH][nb][D] centroid gradients (gk scaled by s)
+  float* gb_;                    // [splits][BH][nb]    centroid-logit gradients
+  float* coef;                   // [3][BH][64 nb]: alpha, beta, gamma of each key row (modes 1, 2)
+  float* da_part;                // [BH][nb][D] (modes 1, 2)
+  float* da;                     // [BH][D] anchor gradient over its row count (modes 1, 2)
+  int* status;
+};
+int attn_bwd_splits(int nb);
+cudaError_t launch_attn_bwd(const BwdArgs& a, int D, cudaStream_t st);
+
+// ---- norm of queries and keys with the position rotation ----------------------------------------
+struct NormRopeArgs {
+  const __nv_bfloat16* x[2];     // q, k
+  const __nv_bfloat16* dz[2];    // gradients of the turned rows (backward)
+  __nv_bfloat16* y[2];           // outputs: turned rows (forward), dq and dk (backward)
+  int64_t sb, sn, sh;            // strides of x
+  int64_t gb, gn, gh;            // strides of dq and dk (backward)
+  int64_t ob, on, oh;            // strides of y (forward) or dz (backward)
+  const void* w[2]; int w_bf16;
+  float eps;
+  int half, inter;               // rot_dim / 2; interleaved pairs
+  const float* cos; const float* sin;
+  int64_t tb, tn;                // strides of the tables
+  int B, N, H;
+  float* dw_part;                // [2][norm_rope_parts][D]
+  float* dw[2];
+};
+int norm_rope_parts(int B, int N, int H, int D);   // CTAs a tensor of the backward kernel
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int D, cudaStream_t st);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, int D, cudaStream_t st);
 
 }  // namespace sol

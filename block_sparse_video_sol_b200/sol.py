@@ -26,7 +26,9 @@ SOL_OK, SOL_ERR_INVALID_ARG, SOL_ERR_UNSUPPORTED, SOL_ERR_WORKSPACE, SOL_ERR_CUD
 EXPORTS = ("sol_workspace_bytes", "sol_workspace_offsets", "sol_workspace_int8_offsets", "sol_col_capacity", "sol_pool", "sol_route", "sol_route_static",
            "sol_attn_fwd", "sol_forward_host", "sol_host_staging_bytes", "sol_last_device_status",
            "sol_status_string", "sol_last_error_text", "sol_debug_drop_arrive",
-           "sol_reblock_workspace_bytes", "sol_reblock", "sol_gather_rows", "sol_scatter_rows")
+           "sol_reblock_workspace_bytes", "sol_reblock", "sol_gather_rows", "sol_scatter_rows",
+           "sol_attn_bwd_workspace_bytes", "sol_attn_bwd", "sol_qk_norm_rope",
+           "sol_qk_norm_rope_bwd_workspace_bytes", "sol_qk_norm_rope_bwd")
 
 
 class sol_params(ctypes.Structure):
@@ -39,7 +41,16 @@ class sol_params(ctypes.Structure):
                 ("routing", ctypes.c_int32), ("topk_ratio", ctypes.c_float), ("qk_int8", ctypes.c_int32)]
 
 
+class sol_norm_rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_type", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("table_stride_b", ctypes.c_int64), ("table_stride_n", ctypes.c_int64)]
+
+
 _P = ctypes.POINTER(sol_params)
+_NR = ctypes.POINTER(sol_norm_rope)
+_I64P = ctypes.POINTER(ctypes.c_int64)
 _vp = ctypes.c_void_p
 lib.sol_workspace_bytes.argtypes = [_P]
 lib.sol_workspace_bytes.restype = ctypes.c_size_t
@@ -77,6 +88,17 @@ lib.sol_gather_rows.argtypes = [_P, _vp, _vp, _vp, _vp]
 lib.sol_gather_rows.restype = ctypes.c_int
 lib.sol_scatter_rows.argtypes = [_P, _vp, _vp, _vp, _vp]
 lib.sol_scatter_rows.restype = ctypes.c_int
+lib.sol_attn_bwd_workspace_bytes.argtypes = [_P]
+lib.sol_attn_bwd_workspace_bytes.restype = ctypes.c_size_t
+lib.sol_attn_bwd.argtypes = [_P, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _I64P,
+                             _vp, ctypes.c_size_t, _vp]
+lib.sol_attn_bwd.restype = ctypes.c_int
+lib.sol_qk_norm_rope.argtypes = [_P, _NR, _vp, _vp, _vp, _vp, _vp]
+lib.sol_qk_norm_rope.restype = ctypes.c_int
+lib.sol_qk_norm_rope_bwd_workspace_bytes.argtypes = [_P]
+lib.sol_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+lib.sol_qk_norm_rope_bwd.argtypes = [_P, _NR, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _I64P, _vp, ctypes.c_size_t, _vp]
+lib.sol_qk_norm_rope_bwd.restype = ctypes.c_int
 
 
 class SolError(RuntimeError):
@@ -207,6 +229,83 @@ def sol_attn_fwd(p: sol_params, q, k, v, ws: torch.Tensor, row_ptr: torch.Tensor
                             _ptr(row_ptr), _ptr(col_idx), _ptr(o), _ptr(lse), _stream(stream)), "sol_attn_fwd")
 
 
+def _strides3(strides):
+    return None if strides is None else (ctypes.c_int64 * 3)(*[int(x) for x in strides])
+
+
+def sol_attn_bwd_workspace_bytes(p: sol_params) -> int:
+    return lib.sol_attn_bwd_workspace_bytes(ctypes.byref(p))
+
+
+def sol_attn_bwd(p: sol_params, q, k, v, ws: torch.Tensor, row_ptr: torch.Tensor, col_idx: torch.Tensor,
+                 o: torch.Tensor, lse: torch.Tensor, d_o: torch.Tensor, dq, dk, dv, bws: torch.Tensor,
+                 grad_strides=None, stream=None):
+    """Gradients of sol_attn_fwd into dq, dk, dv (element strides ``grad_strides`` = (b, n, h), or p's
+    in_strides); ws, row_ptr, col_idx, o and lse are the forward's (see include/sol.h)."""
+    _check(lib.sol_attn_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(ws), ws.numel() * ws.element_size(),
+                            _ptr(row_ptr), _ptr(col_idx), _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv),
+                            _strides3(grad_strides), _ptr(bws), bws.numel() * bws.element_size(), _stream(stream)),
+           "sol_attn_bwd")
+
+
+def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                   cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   rot_dim: Optional[int] = None, interleaved: bool = False) -> sol_norm_rope:
+    """Fill a sol_norm_rope (it keeps the tensors alive).
+
+    The weights are [D], both fp32 or both bf16 (None: ones).  cos and sin are fp32
+    [N, rot_dim/2] or [B, N, rot_dim/2] with equal strides and contiguous rows; without them
+    only the norm is applied.  ``rot_dim`` defaults to the tables' width.
+    """
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    for w in weights:
+        if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != weights[0].dtype or not w.is_contiguous():
+            raise ValueError("the weights must be contiguous, both fp32 or both bf16")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    sb = sn = 0
+    if cos is None:
+        if rot_dim:
+            raise ValueError("rot_dim needs the cos and sin tables")
+        rot_dim = 0
+    else:
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.shape != sin.shape or cos.dim() not in (2, 3):
+            raise ValueError("cos and sin must be fp32 tables of one shape, [N, rot_dim/2] or [B, N, rot_dim/2]")
+        rot_dim = 2 * cos.shape[-1] if rot_dim is None else rot_dim
+        if rot_dim != 2 * cos.shape[-1]:
+            raise ValueError(f"rot_dim {rot_dim} needs tables of width {rot_dim // 2}, got {cos.shape[-1]}")
+        if cos.numel() and (cos.stride() != sin.stride() or cos.stride(-1) != 1):
+            raise ValueError("cos and sin must have identical strides and contiguous rows")
+        if rot_dim:
+            sn = cos.stride(-2) if cos.shape[-2] > 1 else 0
+            sb = cos.stride(0) if cos.dim() == 3 and cos.shape[0] > 1 else 0
+    nr = sol_norm_rope(_ptr(q_weight), _ptr(k_weight), int(bool(weights) and weights[0].dtype == torch.bfloat16),
+                       float(eps), int(rot_dim), int(bool(interleaved)), _ptr(cos) if rot_dim else None,
+                       _ptr(sin) if rot_dim else None, sb, sn)
+    nr.tensors = (q_weight, k_weight, cos, sin)
+    return nr
+
+
+def sol_qk_norm_rope(p: sol_params, nr: sol_norm_rope, q, k, qo, ko, stream=None):
+    """RMS norm per head and position rotation of q and k (p's in_strides) into qo and ko (p's out_strides)."""
+    _check(lib.sol_qk_norm_rope(ctypes.byref(p), ctypes.byref(nr), _ptr(q), _ptr(k), _ptr(qo), _ptr(ko),
+                                _stream(stream)), "sol_qk_norm_rope")
+
+
+def sol_qk_norm_rope_bwd_workspace_bytes(p: sol_params) -> int:
+    return lib.sol_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
+
+
+def sol_qk_norm_rope_bwd(p: sol_params, nr: sol_norm_rope, q, k, dqo, dko, dq, dk, dq_weight: Optional[torch.Tensor],
+                         dk_weight: Optional[torch.Tensor], ws: torch.Tensor, grad_strides=None, stream=None):
+    """Gradient of sol_qk_norm_rope: dqo, dko (p's out_strides) into dq, dk (``grad_strides``, or p's
+    in_strides) and the fp32 weight gradients (each may be None)."""
+    _check(lib.sol_qk_norm_rope_bwd(ctypes.byref(p), ctypes.byref(nr), _ptr(q), _ptr(k), _ptr(dqo), _ptr(dko),
+                                    _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _strides3(grad_strides),
+                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "sol_qk_norm_rope_bwd")
+
+
 def sol_last_device_status(stream=None):
     _check(lib.sol_last_device_status(_stream(stream)), "device status")
 
@@ -286,12 +385,12 @@ class ReblockBuffers:
     buf: Buffers
 
 
-def alloc_reblock(p: sol_params, device) -> ReblockBuffers:
+def alloc_reblock(p: sol_params, device, with_lse: bool = False) -> ReblockBuffers:
     hm = head_major_params(p)
     ws = torch.empty(max(1, sol_reblock_workspace_bytes(p)), dtype=torch.uint8, device=device)
     perm = torch.empty(max(1, p.B * p.H * p.N), dtype=torch.int32, device=device)
     qp, kp, vp = (torch.empty((p.B, p.H, p.N, p.D), dtype=torch.bfloat16, device=device) for _ in range(3))
-    return ReblockBuffers(ws, perm, qp, kp, vp, hm, alloc_buffers(hm, device, head_major_out=True))
+    return ReblockBuffers(ws, perm, qp, kp, vp, hm, alloc_buffers(hm, device, with_lse, head_major_out=True))
 
 
 def forward_reblocked(p: sol_params, q, k, v, o: torch.Tensor, rb: ReblockBuffers, stream=None):
@@ -310,6 +409,143 @@ def forward(p: sol_params, q, k, v, buf: Buffers, stream=None) -> Buffers:
     sol_route(p, buf.ws, buf.row_ptr, buf.col_idx, stream)
     sol_attn_fwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse, stream)
     return buf
+
+
+@dataclass
+class GradBuffers:
+    """Caller-owned buffers of one backward pass: its workspace and the gradients
+    (contiguous [B, N, H, D], element strides ``strides``)."""
+    ws: torch.Tensor
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+    strides: tuple
+
+
+def alloc_grads(p: sol_params, device) -> GradBuffers:
+    ws = torch.empty(max(1, sol_attn_bwd_workspace_bytes(p)), dtype=torch.uint8, device=device)
+    dq, dk, dv = (torch.empty((p.B, p.N, p.H, p.D), dtype=torch.bfloat16, device=device) for _ in range(3))
+    return GradBuffers(ws, dq, dk, dv, (p.N * p.H * p.D, p.H * p.D, p.D))
+
+
+def backward(p: sol_params, q, k, v, buf: Buffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
+    """Enqueue the gradient of ``forward`` (buf as it left it, with an lse) for d_o (p's out_strides)."""
+    if buf.lse is None:
+        raise ValueError("the backward pass needs the forward's lse (alloc_buffers(with_lse=True))")
+    sol_attn_bwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse, d_o, g.dq, g.dk, g.dv, g.ws, g.strides,
+                 stream)
+    return g
+
+
+def backward_reblocked(p: sol_params, rb: ReblockBuffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
+    """Gradient of ``forward_reblocked`` (rb as it left it, with an lse) for d_o laid out as p's
+    in_strides: gather d_o into the partition's order, the backward pass there, scatter the three
+    gradients back into ``g`` (g.ws from alloc_grads of the same shape)."""
+    if rb.buf.lse is None:
+        raise ValueError("the backward pass needs the forward's lse (alloc_reblock(with_lse=True))")
+    hm = (p.H * p.N * p.D, p.D, p.N * p.D)
+    dop, dqp, dkp, dvp = (torch.empty_like(rb.qp) for _ in range(4))
+    sol_gather_rows(p, rb.perm, d_o, dop, stream)
+    sol_attn_bwd(rb.hm, rb.qp, rb.kp, rb.vp, rb.buf.ws, rb.buf.row_ptr, rb.buf.col_idx, rb.buf.o, rb.buf.lse, dop, dqp,
+                 dkp, dvp, g.ws, hm, stream)
+    to = make_params(p.B, p.N, p.H, p.D, prefix_len=p.prefix_len, out_strides=g.strides)
+    for src, dst in ((dqp, g.dq), (dkp, g.dk), (dvp, g.dv)):
+        sol_scatter_rows(to, rb.perm, src, dst, stream)
+    return g
+
+
+def _like_output(d_o: torch.Tensor) -> torch.Tensor:
+    """An incoming gradient as the kernels read it: bf16, contiguous, 16-byte aligned."""
+    d_o = d_o.to(torch.bfloat16).contiguous()
+    return d_o if d_o.data_ptr() % 16 == 0 else d_o.clone()
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, p):
+        with torch.cuda.device(q.device):
+            buf = alloc_buffers(p, q.device, with_lse=True)
+            forward(p, q, k, v, buf)
+        ctx.p = p
+        ctx.save_for_backward(q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
+        return buf.o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_o):
+        q, k, v, ws, row_ptr, col_idx, o, lse = ctx.saved_tensors
+        with torch.cuda.device(q.device):
+            g = alloc_grads(ctx.p, q.device)
+            sol_attn_bwd(ctx.p, q, k, v, ws, row_ptr, col_idx, o, lse, _like_output(d_o), g.dq, g.dk, g.dv, g.ws,
+                         g.strides)
+        return g.dq, g.dk, g.dv, None
+
+
+def _check_bthd(tensors, what: str):
+    for t in tensors:
+        if (t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4 or t.stride(3) != 1
+                or t.shape != tensors[0].shape or t.stride() != tensors[0].stride() or t.device != tensors[0].device):
+            raise ValueError(f"{what} must be bf16 CUDA tensors [B, N, H, D] on one device with identical shapes and "
+                             "strides and contiguous head dim")
+
+
+def differentiable_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tau: float = 1.0, prefix_len: int = 0,
+                             log_mass_bias: int = 0, scale: float = 0.0, topk_ratio: Optional[float] = None,
+                             compressed: bool = False) -> torch.Tensor:
+    """``attention`` for autograd: returns o [B, N, H, D], whose backward runs sol_attn_bwd on the
+    forward's lists.  The workspace and lists of the call are kept until the backward pass."""
+    _check_bthd((q, k, v), "q, k, v")
+    B, N, H, D = q.shape
+    p = make_params(B, N, H, D, tau, prefix_len, log_mass_bias, scale, in_strides=q.stride()[:3],
+                    topk_ratio=topk_ratio, compressed=compressed)
+    return _Attention.apply(q, k, v, p)
+
+
+class _QKNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, eps, interleaved):
+        B, N, H, D = q.shape
+        ctx.p = make_params(B, N, H, D, in_strides=q.stride()[:3])
+        ctx.nr = make_norm_rope(q_weight, k_weight, cos, sin, eps, interleaved=interleaved)
+        ctx.wdtype = [None if w is None else w.dtype for w in (q_weight, k_weight)]
+        with torch.cuda.device(q.device):
+            qo, ko = (torch.empty((B, N, H, D), dtype=q.dtype, device=q.device) for _ in range(2))
+            sol_qk_norm_rope(ctx.p, ctx.nr, q, k, qo, ko)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin)   # version checks; ctx.nr holds their addresses
+        return qo, ko
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dqo, dko):
+        q, k = ctx.saved_tensors[:2]
+        p = ctx.p
+        with torch.cuda.device(q.device):
+            dq, dk = (torch.empty((p.B, p.N, p.H, p.D), dtype=q.dtype, device=q.device) for _ in range(2))
+            dw = [torch.zeros(p.D, device=q.device) if t is not None and ctx.needs_input_grad[2 + i] else None
+                  for i, t in enumerate(ctx.wdtype)]
+            ws = torch.empty(max(1, sol_qk_norm_rope_bwd_workspace_bytes(p)), dtype=torch.uint8, device=q.device)
+            sol_qk_norm_rope_bwd(p, ctx.nr, q, k, _like_output(dqo), _like_output(dko), dq, dk, *dw, ws,
+                                 grad_strides=(p.N * p.H * p.D, p.H * p.D, p.D))
+        dw = [None if g is None else g.to(t) for g, t in zip(dw, ctx.wdtype)]
+        return dq, dk, *dw, None, None, None, None
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                 cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """RMS norm of every query and key head and the position rotation, for autograd.
+
+    q, k are bf16 CUDA tensors [B, N, H, D] (views of the fused projection allowed); weights and
+    tables as for make_norm_rope.  Returns new contiguous (q, k)."""
+    _check_bthd((q, k), "q, k")
+    B, N, H, D = q.shape
+    for w in (q_weight, k_weight):
+        if w is not None and (w.shape != (D,) or w.device != q.device):
+            raise ValueError("the weights must have the head dimension's length and q's device")
+    if cos is not None and (cos.shape[-2] != N or (cos.dim() == 3 and cos.shape[0] not in (1, B))
+                            or cos.device != q.device or sin.device != q.device):
+        raise ValueError("the tables must cover q's positions (and batch) on its device")
+    return _QKNormRope.apply(q, k, q_weight, k_weight, cos, sin, eps, interleaved)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tau: float = 1.0, prefix_len: int = 0,

@@ -10,6 +10,10 @@
  *   sol_attn_fwd  exact attention over the listed key blocks, one centroid
  *                 term per unlisted block, merged in one fp32 online softmax
  *
+ * For training, sol_attn_bwd gives the gradients of that pass, and
+ * sol_qk_norm_rope / sol_qk_norm_rope_bwd norm and turn the queries and keys
+ * in front of it.
+ *
  * Method sources (web pages; no code or equations are published):
  *   - Star7 README "MiniMax H3 Activation Chunk & Attention Acceleration",
  *     section 工作原理 > Sol: Q64/K64 blocks, tau = 1.0 threshold routing;
@@ -295,6 +299,78 @@ sol_status sol_reblock(const sol_params* p, const void* q, const void* k, void* 
 sol_status sol_gather_rows(const sol_params* p, const int32_t* perm, const void* x, void* xp, void* stream);
 /* x[b, perm[b, h, pos], h, :] = xp[b, h, pos, :]  (x strided by out_stride_*) */
 sol_status sol_scatter_rows(const sol_params* p, const int32_t* perm, const void* xp, void* x, void* stream);
+
+/* ---- Training -----------------------------------------------------------
+ * The method's pages describe inference only; these entry points have no
+ * counterpart there.
+ *
+ * sol_attn_bwd: gradients of sol_attn_fwd with respect to Q, K and V for given
+ * lists (the routing is a constant), recomputing the probabilities.
+ *   q, k, v, ws, row_ptr, col_idx  as given to sol_attn_fwd (ws is only read;
+ *            it must still hold what sol_pool wrote for these q, k, v).
+ *   o, lse   sol_attn_fwd's outputs; d_o the gradient of o.  o and d_o have
+ *            strides p->out_stride_* (0 repeats, e.g. an expanded gradient).
+ *   dq, dk, dv  bf16 device, written (rows < N): strides g_strides[3] = {b, n,
+ *            h} in elements, or p->in_stride_* if g_strides is NULL.  Every
+ *            (b, n, h) must be a row of its own, or SOL_ERR_INVALID_ARG.
+ *   bws      device workspace of bws_bytes >= sol_attn_bwd_workspace_bytes(p),
+ *            256-byte aligned; nothing in it outlives the call.
+ * The gradient runs through the exact terms and through the centroid terms
+ * into the rows that were pooled: block means (log_mass_bias 0), the
+ * log-mass bias and its anchor (1), the weighted summaries (2); the rounding of
+ * the centroids to bf16 is passed straight through.  A row whose lists are
+ * empty and that has no centroid terms (routing 1) gets dq = 0.  A non-finite
+ * row of K or V reaches every query row of a 128-row tile that takes its key
+ * block, as in sol_attn_fwd; one of Q or dO every key row of a 128-row tile.
+ * No atomics: the same inputs give the same bits.  qk_int8 = 1:
+ * SOL_ERR_UNSUPPORTED (its codes have no gradient). */
+size_t sol_attn_bwd_workspace_bytes(const sol_params* p);
+sol_status sol_attn_bwd(const sol_params* p, const void* q, const void* k, const void* v, const void* ws,
+                        size_t ws_bytes, const int32_t* row_ptr, const int32_t* col_idx, const void* o,
+                        const float* lse, const void* d_o, void* dq, void* dk, void* dv, const int64_t* g_strides,
+                        void* bws, size_t bws_bytes, void* stream);
+
+/* What sol_qk_norm_rope applies to every query and key head. */
+typedef struct {
+  const void* q_weight;      /* [D] device, 16-byte aligned, or NULL (ones) */
+  const void* k_weight;
+  int32_t weight_type;       /* 0 fp32, 1 bf16 (both weights) */
+  float eps;                 /* added to the mean square; finite and >= 0 */
+  int32_t rot_dim;           /* leading dims that are turned: a multiple of 16 in [0, D]; 0: norm only */
+  int32_t interleaved;       /* pairs of turned dims: 0 (i, i + rot_dim/2), 1 (2i, 2i + 1) */
+  const float* cos;          /* [B or 1, N, rot_dim/2] device, 16-byte aligned; unused if rot_dim is 0 */
+  const float* sin;
+  int64_t table_stride_b;    /* element strides of both tables, multiples of 4; b: 0 shares one table */
+  int64_t table_stride_n;
+} sol_norm_rope;
+
+/* sol_qk_norm_rope: RMS norm of every query and key head and the position
+ * rotation in one pass.  Per row x: y = x / sqrt(mean x^2 + eps) * weight, then
+ * the pairs (a, b) of the turned dims become (a cos - b sin, b cos + a sin);
+ * fp32 inside, rounded once.
+ *   q, k     [B, N, H, D] bf16, strides p->in_stride_* (e.g. views of the fused
+ *            QKV projection);  qo, ko  the same shape, strides p->out_stride_*,
+ *            distinct rows.  qo = q and ko = k in place is allowed with equal
+ *            strides; other overlaps are not.
+ * Fields of p used: B, N, H, D and the strides; the others must pass the common
+ * validation. */
+sol_status sol_qk_norm_rope(const sol_params* p, const sol_norm_rope* nr, const void* q, const void* k, void* qo,
+                            void* ko, void* stream);
+
+/* sol_qk_norm_rope_bwd: its gradient.
+ *   q, k     the forward's inputs (strides p->in_stride_*);  dqo, dko  the
+ *            gradients of its outputs (strides p->out_stride_*).
+ *   dq, dk   written: strides g_strides[3], or p->in_stride_* if NULL; distinct
+ *            rows.  May be dqo and dko themselves (equal strides).
+ *   dq_weight, dk_weight  fp32 [D] device, 16-byte aligned, written; each may be
+ *            NULL.
+ *   ws       device workspace, 256-byte aligned, of at least
+ *            sol_qk_norm_rope_bwd_workspace_bytes(p) bytes.
+ * The weights' gradients are summed in a fixed order. */
+size_t sol_qk_norm_rope_bwd_workspace_bytes(const sol_params* p);
+sol_status sol_qk_norm_rope_bwd(const sol_params* p, const sol_norm_rope* nr, const void* q, const void* k,
+                                const void* dqo, const void* dko, void* dq, void* dk, float* dq_weight,
+                                float* dk_weight, const int64_t* g_strides, void* ws, size_t ws_bytes, void* stream);
 
 /* Fault injection for testing the bounded waits (the device-side failure
  * path).  Only a library built with SOL_FAULT_TEST (libsol_fault.so, whose

@@ -1,0 +1,438 @@
+"""Gradients on the GPU: sol_attn_bwd and sol_qk_norm_rope(_bwd) against the fp64
+formulas of oracle/train_ref.py, element by element.
+
+sol_attn_bwd is given what the forward left (o, lse, lists, centroid operands);
+every element of dq, dk, dv has to lie within the bound that attention_backward
+derives from the roundings of p, ds and the outputs to bf16 (2^-8 each) and from
+fp32 sums.  The norm's outputs are fp32 inside and rounded once: 2^-8 of the
+value plus 2^-18 of the magnitudes that it is the sum of (a dozen fp32 steps and
+a reciprocal square root of two units in the last place).
+"""
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_video_sol_b200 import synth
+from oracle import sol_ref, train_ref
+from tests import parity
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def sol():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from block_sparse_video_sol_b200 import build
+    build.build()
+    from block_sparse_video_sol_b200 import sol as mod
+    return mod
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def inputs(B, N, H, D, seed, gain=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda: torch.randn(B, N, H, D, generator=g, device="cuda")
+    topic = torch.randn(B, -(-N // 32), H, D, generator=g, device="cuda").repeat_interleave(32, 1)[:, :N]
+    return [(gain * (topic + r())).bfloat16() for _ in range(2)] + [r().bfloat16(), r().bfloat16()]
+
+
+def check_grads(sol, p, buf, q, k, v, do, grads):
+    """dq, dk, dv ([B, N, H, D]) of every head within the derived bounds."""
+    _, _, mask = parity.gpu_mask(p, buf)
+    w = sol.workspace_views(p, buf.ws)
+    cent = p.routing != 1
+    worst = 0.0
+    for b in range(p.B):
+        for h in range(p.H):
+            want = train_ref.attention_backward(
+                *(f64(x[b, :, h]) for x in (q, k, v, do, buf.o)), f64(buf.lse[b, h]), mask[b, h],
+                f64(w["kbar16"][b, h]), f64(w["vbar16"][b, h]), f64(w["cbias"][b, h]), p.prefix_len, p.log_mass_bias,
+                cent, p.scale or None)
+            for name, got, (g, bound) in zip(("dq", "dk", "dv"), grads, want):
+                x = f64(got[b, :, h])
+                assert np.isfinite(x).all(), (name, b, h)
+                ratio = (np.abs(x - g) / bound).max()
+                assert ratio <= 1.0, (name, b, h, ratio, np.unravel_index((np.abs(x - g) / bound).argmax(), g.shape))
+                worst = max(worst, ratio)
+    return worst
+
+
+def run(sol, B, N, H, D, seed=0, gain=1.0, **kw):
+    q, k, v, do = inputs(B, N, H, D, seed, gain)
+    p = sol.make_params(B, N, H, D, **kw)
+    buf = sol.alloc_buffers(p, q.device, with_lse=True)
+    sol.forward(p, q, k, v, buf)
+    g = sol.alloc_grads(p, q.device)
+    for t in (g.dq, g.dk, g.dv):
+        t.fill_(float("nan"))
+    g.ws.fill_(255)   # whatever the workspace held
+    sol.backward(p, q, k, v, buf, do, g)
+    sol.sol_last_device_status()
+    return p, buf, (q, k, v, do), g
+
+
+ROUTES = [dict(tau=0.5), dict(tau=0.5, log_mass_bias=1), dict(tau=0.5, log_mass_bias=2), dict(topk_ratio=0.3),
+          dict(topk_ratio=0.2, compressed=True, log_mass_bias=2)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N", [1, 5, 63, 64, 65, 128, 129, 200])
+@pytest.mark.parametrize("route", range(5))
+def test_short_lengths(sol, N, D, route):
+    p, buf, (q, k, v, do), g = run(sol, 1, N, 2, D, seed=N, **ROUTES[route])
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("route", range(5))
+@pytest.mark.parametrize("B,N,H,prefix", [(2, 1000, 3, 100), (1, 777, 2, 13), (1, 2113, 1, 0), (1, 640, 1, 640)])
+def test_ragged_lengths_and_prefixes(sol, B, N, H, prefix, route, D):
+    p, buf, (q, k, v, do), g = run(sol, B, N, H, D, seed=N, prefix_len=prefix, **ROUTES[route])
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+
+
+@pytest.mark.parametrize("mode", [0, 2])
+def test_every_centroid_range_and_long_lists(sol, mode):
+    """N = 9,000: 141 blocks, eight query ranges of the centroid pass, several bitmap words."""
+    p, buf, (q, k, v, do), g = run(sol, 1, 9000, 1, 128, seed=3, prefix_len=70, log_mass_bias=mode, tau=0.8)
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+
+
+def test_all_blocks_exact_and_no_block_exact(sol):
+    p, buf, (q, k, v, do), g = run(sol, 1, 500, 2, 128, tau=-float("inf"))
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+    p, buf, (q, k, v, do), g = run(sol, 1, 500, 2, 128, tau=50.0)
+    assert int(buf.row_ptr[-1]) == 0
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+
+
+def test_large_logits_and_a_scale_of_its_own(sol):
+    """Logits of +-100: the softmax is nearly one-hot and the saved normaliser far from zero."""
+    p, buf, (q, k, v, do), g = run(sol, 1, 300, 2, 64, seed=9, gain=5.0, scale=0.3, tau=0.3, log_mass_bias=1)
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+
+
+def test_empty_rows_and_repeated_entries(sol):
+    """Caller's lists under routing 1: a tile without keys (its o and lse are never written), a tile with one
+    empty half, a key block that nobody lists, and an entry listed twice."""
+    B, N, H, D = 1, 64 * 6 + 10, 1, 128
+    q, k, v, do = inputs(B, N, H, D, 4)
+    p = sol.make_params(B, N, H, D, topk_ratio=0.3)
+    buf = sol.alloc_buffers(p, q.device, with_lse=True)
+    sol.sol_pool(p, q, k, v, buf.ws)
+    lists = [[], [], [1, 1, 4], [], [0, 6], [2], [6]]
+    buf.row_ptr.copy_(torch.tensor(np.cumsum([0] + [len(x) for x in lists]), dtype=torch.int32))
+    flat = torch.tensor(sum(lists, []), dtype=torch.int32, device="cuda")
+    buf.col_idx[:len(flat)] = flat
+    buf.o.fill_(float("nan"))
+    buf.lse.fill_(float("nan"))
+    sol.sol_attn_fwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
+    g = sol.alloc_grads(p, q.device)
+    sol.backward(p, q, k, v, buf, do, g)
+    sol.sol_last_device_status()
+    assert (g.dq[:, :128] == 0).all() and (g.dq[:, 192:256] == 0).all()
+    for j in (3, 5):
+        assert (g.dk[:, 64 * j:64 * (j + 1)] == 0).all() and (g.dv[:, 64 * j:64 * (j + 1)] == 0).all()
+    # the oracle's lse of the empty rows: no terms
+    rows = torch.zeros(N, dtype=torch.bool)
+    rows[:128] = rows[192:256] = True
+    buf.lse[:, :, rows] = -float("inf")
+    buf.o[:, rows] = 0
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+
+
+def test_bad_list_entry_is_reported_and_skipped(sol):
+    p, buf, (q, k, v, do), g = run(sol, 1, 300, 1, 64, topk_ratio=0.4)
+    want = [t.clone() for t in (g.dq, g.dk, g.dv)]
+    n = int(buf.row_ptr[-1])
+    rp, ci = buf.row_ptr.clone(), buf.col_idx.clone()
+    rp[-1] += 2
+    ci = torch.cat([ci[:n], torch.tensor([5, -1], dtype=torch.int32, device="cuda")])
+    sol.sol_attn_bwd(p, q, k, v, buf.ws, rp, ci, buf.o, buf.lse, do, g.dq, g.dk, g.dv, g.ws)
+    with pytest.raises(sol.SolError):
+        sol.sol_last_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(want, (g.dq, g.dk, g.dv)))
+
+
+def test_strided_views_head_runs_and_repeats_are_bit_identical(sol):
+    B, N, H, D = 2, 700, 4, 128
+    kw = dict(prefix_len=40, log_mass_bias=2, tau=0.5)
+    q, k, v, do = inputs(B, N, H, D, 6)
+    p = sol.make_params(B, N, H, D, **kw)
+    buf = sol.alloc_buffers(p, "cuda", with_lse=True)
+    sol.forward(p, q, k, v, buf)
+    g = sol.alloc_grads(p, "cuda")
+    sol.backward(p, q, k, v, buf, do, g)
+    want = [t.clone() for t in (g.dq, g.dk, g.dv)]
+    sol.backward(p, q, k, v, buf, do, g)
+    assert all(torch.equal(a, b) for a, b in zip(want, (g.dq, g.dk, g.dv)))
+
+    # views of fused projections in and out; an output gradient with strides of its own
+    qkv = torch.stack((q, k, v), 2)
+    dqkv = torch.full_like(qkv, float("nan"))
+    views, gviews = qkv.unbind(2), dqkv.unbind(2)
+    o3, do3 = (torch.empty(B, N, 2, H, D, dtype=q.dtype, device="cuda")[:, :, 1] for _ in range(2))
+    o3.copy_(buf.o)
+    do3.copy_(do)
+    p2 = sol.make_params(B, N, H, D, in_strides=views[0].stride()[:3], out_strides=o3.stride()[:3], **kw)
+    sol.sol_attn_bwd(p2, *views, buf.ws, buf.row_ptr, buf.col_idx, o3, buf.lse, do3, *gviews, g.ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, gviews))
+
+    # heads 1 and 2 alone (the other heads' gradients stay as they were)
+    sub = sol.make_params(B, N, 2, D, in_strides=q.stride()[:3], out_strides=q.stride()[:3], **kw)
+    h12 = [t[:, :, 1:3] for t in (q, k, v)]
+    b2 = sol.alloc_buffers(sub, "cuda")
+    lse2 = torch.empty(B, 2, N, device="cuda")
+    b2.o = torch.empty_like(q)[:, :, 1:3]
+    sol.sol_pool(sub, *h12, b2.ws)
+    sol.sol_route(sub, b2.ws, b2.row_ptr, b2.col_idx)
+    sol.sol_attn_fwd(sub, *h12, b2.ws, b2.row_ptr, b2.col_idx, b2.o, lse2)
+    part = [torch.full_like(t, 7.0) for t in want]
+    ws2 = torch.empty(sol.sol_attn_bwd_workspace_bytes(sub), dtype=torch.uint8, device="cuda")
+    sol.sol_attn_bwd(sub, *h12, b2.ws, b2.row_ptr, b2.col_idx, b2.o, lse2, do[:, :, 1:3], *(t[:, :, 1:3] for t in part), ws2)
+    torch.cuda.synchronize()
+    for a, b in zip(want, part):
+        assert torch.equal(a[:, :, 1:3], b[:, :, 1:3]) and (b[:, :, 0] == 7).all() and (b[:, :, 3] == 7).all()
+
+
+def test_rows_past_the_last_are_left_alone(sol):
+    B, N, H, D = 1, 130, 2, 64
+    big = [torch.randn(B, 200, H, D, device="cuda").bfloat16() for _ in range(4)]
+    for t in big:
+        t[:, N:] = float("nan")
+    q, k, v, do = (t[:, :N] for t in big)
+    p = sol.make_params(B, N, H, D, tau=0.2)
+    buf = sol.alloc_buffers(p, "cuda", with_lse=True)
+    sol.forward(p, q, k, v, buf)
+    grads = [torch.full_like(t, 3.0) for t in big[:3]]
+    g = sol.alloc_grads(p, "cuda")
+    sol.sol_attn_bwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse, do, *grads, g.ws)
+    torch.cuda.synchronize()
+    assert all((t[:, N:] == 3).all() for t in grads)
+    check_grads(sol, p, buf, q, k, v, do, [t[:, :N] for t in grads])
+
+
+def test_reblocked_backward(sol):
+    w = synth.tiny()
+    q, k, v = (parity.to_dev(x) for x in synth.generate(w))
+    do = torch.randn_like(q)
+    p = sol.make_params(w.B, w.N, w.H, w.D, tau=w.tau)
+    rb = sol.alloc_reblock(p, "cuda", with_lse=True)
+    sol.forward_reblocked(p, q, k, v, torch.empty_like(q), rb)
+    g = sol.alloc_grads(p, "cuda")
+    sol.backward_reblocked(p, rb, do, g)
+    sol.sol_last_device_status()
+    at = rb.perm.long().view(w.B, w.H, w.N)
+    # the gradients in the partition's order against the oracle on the permuted rows
+    perm = lambda t: torch.stack([t[0, at[0, h], h] for h in range(w.H)], 1)[None]
+    bthd = lambda t: t.view(w.B, w.H, w.N, w.D).transpose(1, 2)
+    buf = sol.Buffers(rb.buf.ws, rb.buf.row_ptr, rb.buf.col_idx, bthd(rb.buf.o), rb.buf.lse)
+    check_grads(sol, p, buf, *(perm(t) for t in (q, k, v, do)), [perm(t) for t in (g.dq, g.dk, g.dv)])
+
+
+# ---- norm of queries and keys with rotation -------------------------------------------------------
+def rope_inputs(B, N, H, D, rot, weights, tables_b, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    q, k = ((r(B, N, H, D) * (1 + 3 * r(1, 1, H, 1).abs())).bfloat16() for _ in range(2))
+    w = [None, None] if weights is None else [(1 + 0.2 * r(D)).to(weights) for _ in range(2)]
+    ang = 100 * r(tables_b, N, rot // 2) if tables_b else 100 * r(N, rot // 2)
+    return q, k, w, ang.cos().contiguous(), ang.sin().contiguous(), r(B, N, H, D).bfloat16(), r(B, N, H, D).bfloat16()
+
+
+@pytest.mark.parametrize("D,rot", [(64, 64), (64, 32), (64, 0), (128, 128), (128, 48), (128, 16)])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("B,N,H,weights,tables_b", [(1, 1, 56, torch.bfloat16, 0), (8, 1, 5, torch.float32, 8),
+                                                    (2, 77, 3, torch.float32, 0), (3, 130, 9, None, 3),
+                                                    (1, 1025, 17, torch.bfloat16, 1)])
+def test_norm_rope_forward_and_backward(sol, B, N, H, weights, tables_b, inter, D, rot):
+    q, k, w, cos, sin, dqo, dko = rope_inputs(B, N, H, D, rot, weights, tables_b, N + rot)
+    eps = 1e-5
+    p = sol.make_params(B, N, H, D)
+    nr = sol.make_norm_rope(*w, cos, sin, eps, interleaved=inter)
+    qo, ko, dq, dk = (torch.full_like(q, float("nan")) for _ in range(4))
+    dw = [torch.full((D,), float("nan"), device="cuda") for _ in range(2)]
+    ws = torch.full((sol.sol_qk_norm_rope_bwd_workspace_bytes(p),), 255, dtype=torch.uint8, device="cuda")
+    sol.sol_qk_norm_rope(p, nr, q, k, qo, ko)
+    sol.sol_qk_norm_rope_bwd(p, nr, q, k, dqo, dko, dq, dk, *dw, ws)
+    torch.cuda.synchronize()
+    c, s = (f64(t).reshape(tables_b or 1, N, rot // 2) for t in (cos, sin))
+    for x, wt, y, dz, dx, g in ((q, w[0], qo, dqo, dq, dw[0]), (k, w[1], ko, dko, dk, dw[1])):
+        wd = np.ones(D) if wt is None else f64(wt)
+        want = train_ref.norm_rope(f64(x), wd, c, s, eps, inter)
+        size = train_ref.rotate(np.abs(f64(x)) * wd, np.abs(c), -np.abs(s), inter)
+        size = np.maximum(size, train_ref.rotate(np.abs(f64(x)) * wd, np.abs(c), np.abs(s), inter))
+        size /= np.sqrt((f64(x) ** 2).mean(-1, keepdims=True))
+        assert (np.abs(f64(y) - want) <= U * np.abs(want) + 2.0 ** -18 * np.abs(size) + 1e-30).all()
+        ex, ew, mag = train_ref.norm_rope_backward(f64(x), wd, c, s, eps, inter, f64(dz))
+        r = 1 / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True))
+        big = np.sqrt((f64(dz) ** 2).sum(-1, keepdims=True)) * wd.max() * r * (1 + np.abs(f64(x)) * r)
+        assert (np.abs(f64(dx) - ex) <= U * np.abs(ex) + 2.0 ** -18 * big + 1e-30).all()
+        # the weight's gradient: chains of at most a few hundred fp32 additions
+        assert (np.abs(g.cpu().numpy() - ew) <= 2.0 ** -24 * 600 * mag + 1e-30).all()
+
+
+def test_norm_rope_in_place_strided_and_null_weight_gradients(sol):
+    B, N, H, D = 2, 300, 5, 128
+    q, k, w, cos, sin, dqo, dko = rope_inputs(B, N, H, D, 128, torch.float32, 0, 1)
+    p = sol.make_params(B, N, H, D)
+    nr = sol.make_norm_rope(*w, cos, sin)
+    qo, ko, dq, dk = (torch.empty_like(q) for _ in range(4))
+    dw = [torch.empty(D, device="cuda") for _ in range(2)]
+    ws = torch.empty(sol.sol_qk_norm_rope_bwd_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    sol.sol_qk_norm_rope(p, nr, q, k, qo, ko)
+    sol.sol_qk_norm_rope_bwd(p, nr, q, k, dqo, dko, dq, dk, *dw, ws)
+    # in place on the fused projection: v untouched, the same bits
+    qkv = torch.stack((q, k, torch.full_like(q, 5.0)), 2)
+    qv, kv, vv = qkv.unbind(2)
+    pv = sol.make_params(B, N, H, D, in_strides=qv.stride()[:3], out_strides=qv.stride()[:3])
+    sol.sol_qk_norm_rope(pv, nr, qv, kv, qv, kv)
+    torch.cuda.synchronize()
+    assert torch.equal(qv, qo) and torch.equal(kv, ko) and (vv == 5).all()
+    # the gradient written over its input, with one weight gradient left out
+    keep = torch.full((D,), 9.0, device="cuda")
+    a, b = dqo.clone(), dko.clone()
+    sol.sol_qk_norm_rope_bwd(p, nr, q, k, a, b, a, b, None, keep, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, dq) and torch.equal(b, dk) and torch.equal(keep, dw[1])
+    sol.sol_qk_norm_rope_bwd(p, nr, q, k, dqo, dko, a, b, None, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, dq)
+    # an expanded incoming gradient (batch and head strides of zero)
+    one = dqo[:1, :, :1]
+    pe = sol.make_params(B, N, H, D, out_strides=(0, one.stride(1), 0))
+    dense = one.expand(B, N, H, D).contiguous()
+    sol.sol_qk_norm_rope_bwd(p, nr, q, k, dense, dense, dq, dk, *dw, ws)
+    sol.sol_qk_norm_rope_bwd(pe, nr, q, k, one, one, a, b, None, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, dq) and torch.equal(b, dk)
+
+
+def test_zero_rows_are_finite(sol):
+    p = sol.make_params(1, 4, 1, 64)
+    z = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    o, ko, dq, dk = (torch.empty_like(z) for _ in range(4))
+    nr = sol.make_norm_rope(None, None)
+    ws = torch.empty(sol.sol_qk_norm_rope_bwd_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    sol.sol_qk_norm_rope(p, nr, z, z, o, ko)
+    sol.sol_qk_norm_rope_bwd(p, nr, z, z, torch.ones_like(z), torch.ones_like(z), dq, dk, None, None, ws)
+    torch.cuda.synchronize()
+    assert (o == 0).all() and torch.isfinite(dq.float()).all()
+
+
+# ---- together ---------------------------------------------------------------------------------------
+def layer(sol, qkv, w, cos, sin, **kw):
+    q, k, v = qkv.unbind(2)
+    q, k = sol.qk_norm_rope(q, k, *w, cos, sin)
+    q.retain_grad()
+    k.retain_grad()
+    return q, k, sol.differentiable_attention(q, k, v.contiguous(), **kw)
+
+
+def test_one_training_step_of_a_layer(sol):
+    """norm + rotation -> pool -> route -> attention and back: the autograd gradients equal the entry points'
+    bit for bit, and both stages' gradients lie within their bounds."""
+    B, N, H, D = 1, 600, 2, 128
+    kw = dict(tau=0.5, prefix_len=20, log_mass_bias=1)
+    q, k, w, cos, sin, do, _ = rope_inputs(B, N, H, D, 128, torch.bfloat16, 0, 2)
+    v = torch.randn_like(q)
+    qkv = torch.stack((q, k, v), 2).requires_grad_()
+    w = [t.requires_grad_() for t in w]
+    qn, kn, o = layer(sol, qkv, w, cos, sin, **kw)
+    o.backward(do)
+    sol.sol_last_device_status()
+    p = sol.make_params(B, N, H, D, **kw)
+    buf = sol.alloc_buffers(p, "cuda", with_lse=True)
+    sol.forward(p, qn.detach(), kn.detach(), v, buf)
+    assert torch.equal(buf.o, o)
+    g = sol.backward(p, qn.detach(), kn.detach(), v, buf, do, sol.alloc_grads(p, "cuda"))
+    assert torch.equal(g.dq, qn.grad) and torch.equal(g.dk, kn.grad) and torch.equal(g.dv, qkv.grad[:, :, 2])
+    check_grads(sol, p, buf, qn.detach(), kn.detach(), v, do, (g.dq, g.dk, g.dv))
+    c, s = f64(cos)[None], f64(sin)[None]
+    for i, (x, wt, dz) in enumerate(((q, w[0], g.dq), (k, w[1], g.dk))):
+        ex, ew, mag = train_ref.norm_rope_backward(f64(x), f64(wt), c, s, 1e-6, False, f64(dz))
+        got = f64(qkv.grad[:, :, i])
+        r = 1 / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True))
+        big = np.sqrt((f64(dz) ** 2).sum(-1, keepdims=True)) * f64(wt).max() * r * (1 + np.abs(f64(x)) * r)
+        assert (np.abs(got - ex) <= U * np.abs(ex) + 2.0 ** -18 * big + 1e-30).all()
+        assert (np.abs(f64(wt.grad) - ew) <= U * np.abs(ew) + 2.0 ** -24 * 600 * mag + 1e-30).all()
+    # a gradient that arrives expanded (o.sum()) and in fp32 arithmetic
+    qkv.grad = None
+    layer(sol, qkv, w, cos, sin, **kw)[2].sum().backward()
+    assert torch.isfinite(qkv.grad.float()).all()
+
+
+def test_two_layers_share_their_input(sol):
+    """Two layers of one fused projection, both backward passes after both forwards: gradients add."""
+    B, N, H, D = 1, 200, 2, 64
+    q, k, w, cos, sin, do, do2 = rope_inputs(B, N, H, D, 64, torch.float32, 0, 3)
+    qkv = torch.stack((q, k, torch.randn_like(q)), 2).requires_grad_()
+    outs = []
+    for use in ((True, False), (False, True), (True, True)):
+        qkv.grad = None
+        a = layer(sol, qkv, w, cos, sin, tau=0.3)[2]
+        b = layer(sol, qkv, w, cos, sin, topk_ratio=0.5)[2]
+        torch.autograd.backward([t for t, u in zip((a, b), use) if u], [d for d, u in zip((do, do2), use) if u])
+        outs.append(qkv.grad.float())
+    want = outs[0] + outs[1]
+    assert ((outs[2] - want).abs() <= U * want.abs() + 1e-30).all()
+
+
+def test_captured_step_replays_on_new_inputs_and_streams(sol):
+    """The whole step captured once on a side stream and replayed; eager calls in between on another stream
+    and with buffers of their own give the same bits."""
+    B, N, H, D = 1, 900, 2, 128
+    kw = dict(tau=0.5, prefix_len=10, log_mass_bias=2)
+
+    def make(seed):
+        q, k, w, cos, sin, do, _ = rope_inputs(B, N, H, D, 128, torch.float32, 0, seed)
+        return [q, k, torch.randn_like(q), do], w, cos, sin
+
+    def bufs():
+        p = sol.make_params(B, N, H, D, **kw)
+        return dict(p=p, buf=sol.alloc_buffers(p, "cuda", with_lse=True), g=sol.alloc_grads(p, "cuda"),
+                    n=[torch.empty(B, N, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(4)],
+                    dw=[torch.empty(D, device="cuda") for _ in range(2)],
+                    ws=torch.empty(sol.sol_qk_norm_rope_bwd_workspace_bytes(p), dtype=torch.uint8, device="cuda"))
+
+    def step(x, nr, s):
+        q, k, v, do = x
+        p, buf, g, n = s["p"], s["buf"], s["g"], s["n"]
+        sol.sol_qk_norm_rope(p, nr, q, k, n[0], n[1])
+        sol.forward(p, n[0], n[1], v, buf)
+        sol.backward(p, n[0], n[1], v, buf, do, g)
+        sol.sol_qk_norm_rope_bwd(p, nr, q, k, g.dq, g.dk, n[2], n[3], *s["dw"], s["ws"])
+
+    result = lambda s: [t.clone() for t in (*s["n"], s["g"].dv, *s["dw"])]
+    x, w, cos, sin = make(1)
+    nr = sol.make_norm_rope(*w, cos, sin)
+    s, other = bufs(), bufs()
+    step(x, nr, s)
+    torch.cuda.synchronize()
+    first = result(s)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(x, nr, s)
+    x2 = make(2)[0]
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+        step(x2, nr, other)
+        want2 = result(other)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, result(s)))
+    for a, b in zip(x, x2):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want2, result(s)))
+    sol.sol_last_device_status()

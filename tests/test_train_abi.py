@@ -1,0 +1,168 @@
+"""Refusals of the training entry points: all synchronous, nothing is launched."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def sol():
+    from block_sparse_video_sol_b200 import build
+    build.build()
+    from block_sparse_video_sol_b200 import sol as mod
+    return mod
+
+
+BIG = 1 << 40
+
+
+def _bwd(sol, p, ptr=4096, ws_bytes=BIG, bws_bytes=BIG, gs=None, **over):
+    names = ["q", "k", "v", "ws", "row_ptr", "col_idx", "o", "lse", "d_o", "dq", "dk", "dv", "bws"]
+    a = {n: over.get(n, ptr) for n in names}
+    g = None if gs is None else (ctypes.c_int64 * 3)(*gs)
+    return sol.lib.sol_attn_bwd(None if p is None else ctypes.byref(p), a["q"], a["k"], a["v"], a["ws"], ws_bytes, a["row_ptr"],
+                                a["col_idx"], a["o"], a["lse"], a["d_o"], a["dq"], a["dk"], a["dv"], g, a["bws"], bws_bytes, None)
+
+
+def _text(sol):
+    return sol.lib.sol_last_error_text().decode()
+
+
+def test_attn_bwd_refusals(sol):
+    p = sol.make_params(2, 1000, 4, 128)
+    assert _bwd(sol, None) == sol.SOL_ERR_INVALID_ARG
+    for name in ("q", "k", "v", "ws", "row_ptr", "col_idx", "o", "lse", "d_o", "dq", "dk", "dv", "bws"):
+        assert _bwd(sol, p, **{name: None}) == sol.SOL_ERR_INVALID_ARG and "NULL" in _text(sol), name
+    for name in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv"):
+        assert _bwd(sol, p, **{name: 4096 + 8}) == sol.SOL_ERR_INVALID_ARG and "aligned" in _text(sol), name
+    for name in ("ws", "bws"):
+        assert _bwd(sol, p, **{name: 4096 + 128}) == sol.SOL_ERR_INVALID_ARG and "256" in _text(sol), name
+    assert _bwd(sol, p, ws_bytes=sol.sol_workspace_bytes(p) - 1) == sol.SOL_ERR_WORKSPACE
+    assert _bwd(sol, p, bws_bytes=sol.sol_attn_bwd_workspace_bytes(p) - 1) == sol.SOL_ERR_WORKSPACE
+    assert _bwd(sol, sol.make_params(2, 1000, 4, 128, qk_int8=True)) == sol.SOL_ERR_UNSUPPORTED
+    assert "INT8" in _text(sol)
+    assert sol.sol_attn_bwd_workspace_bytes(sol.make_params(2, 1000, 4, 128, qk_int8=True)) == 0
+    assert _bwd(sol, sol.make_params(2, 1000, 4, 96)) == sol.SOL_ERR_UNSUPPORTED
+    assert _bwd(sol, sol.make_params(2, 1000, 4, 128, tau=math.nan)) == sol.SOL_ERR_INVALID_ARG
+    # an empty problem enqueues nothing, whatever the pointers
+    assert _bwd(sol, sol.make_params(0, 1000, 4, 128), ptr=None) == sol.SOL_OK
+    assert _bwd(sol, sol.make_params(2, 0, 4, 128), ptr=None) == sol.SOL_OK
+
+
+@pytest.mark.parametrize("gs,ok", [
+    ((512000, 512, 128), True), ((1536000, 1536, 128), True), ((512000, 128, 128000), True), ((1000 * 512 * 3, 1536, 384), True),
+    ((0, 512, 128), False), ((512000, 0, 128), False), ((512000, 512, 0), False), ((512000, 512, 120), False),
+    ((512000, 504, 128), False), ((511992, 512, 128), False), ((512000, 512, 132), False), ((-512000, 512, 128), False)])
+def test_gradient_rows_must_be_distinct(sol, gs, ok):
+    p = sol.make_params(2, 1000, 4, 128)
+    st = _bwd(sol, p, gs=gs, bws_bytes=1)
+    assert st == (sol.SOL_ERR_WORKSPACE if ok else sol.SOL_ERR_INVALID_ARG), _text(sol)
+
+
+def test_broadcast_inputs_need_gradient_strides_of_their_own(sol):
+    p = sol.make_params(2, 1000, 4, 128, in_strides=(0, 512, 128))
+    assert _bwd(sol, p, bws_bytes=1) == sol.SOL_ERR_INVALID_ARG and "overlap" in _text(sol)
+    assert _bwd(sol, p, gs=(512000, 512, 128), bws_bytes=1) == sol.SOL_ERR_WORKSPACE
+    # dims of size one may have any stride
+    assert _bwd(sol, sol.make_params(1, 1000, 1, 128, in_strides=(0, 128, 0)), bws_bytes=1) == sol.SOL_ERR_WORKSPACE
+
+
+def test_attn_bwd_workspace_size(sol):
+    for kw, pooled in ((dict(), 0), (dict(log_mass_bias=2), 1), (dict(topk_ratio=0.2), -1)):
+        p = sol.make_params(1, 32768, 56, 128, **kw)
+        stat = 2 * 56 * 32768 * 4
+        plans = 56 * 256 * ((16 + 2 * 16 + 512) + (16 + 512)) * 4
+        cent = 0 if pooled < 0 else 8 * 56 * 512 * (2 * 128 + 1) * 4
+        rows = 56 * (3 * 32768 + 512 * 128 + 128) * 4 if pooled > 0 else 0
+        got = sol.sol_attn_bwd_workspace_bytes(p)
+        assert stat + plans + cent + rows <= got <= stat + plans + cent + rows + 16 * 256
+    assert sol.sol_attn_bwd_workspace_bytes(sol.make_params(1, 0, 56, 128)) == 0
+
+
+def _nr(sol, **over):
+    f = dict(q_weight=4096, k_weight=4096, weight_type=0, eps=1e-6, rot_dim=64, interleaved=0, cos=4096, sin=4096,
+             table_stride_b=0, table_stride_n=32)
+    f.update(over)
+    return sol.sol_norm_rope(*[f[n] for n, _ in sol.sol_norm_rope._fields_])
+
+
+def _fwd_nr(sol, p, nr, q=4096, k=4096, qo=8192, ko=8192):
+    return sol.lib.sol_qk_norm_rope(ctypes.byref(p), None if nr is None else ctypes.byref(nr), q, k, qo, ko, None)
+
+
+def _bwd_nr(sol, p, nr, gs=None, ws_bytes=BIG, **over):
+    a = {n: over.get(n, 4096) for n in ("q", "k", "dqo", "dko", "dq", "dk", "dqw", "dkw", "ws")}
+    g = None if gs is None else (ctypes.c_int64 * 3)(*gs)
+    return sol.lib.sol_qk_norm_rope_bwd(ctypes.byref(p), None if nr is None else ctypes.byref(nr), a["q"], a["k"],
+                                        a["dqo"], a["dko"], a["dq"], a["dk"], a["dqw"], a["dkw"], g, a["ws"], ws_bytes, None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(weight_type=2), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(rot_dim=8), dict(rot_dim=144),
+    dict(rot_dim=-16), dict(interleaved=2), dict(q_weight=4100), dict(k_weight=4104), dict(cos=None), dict(sin=None),
+    dict(cos=4100), dict(table_stride_n=30), dict(table_stride_b=-32)])
+def test_norm_rope_parameter_refusals(sol, over):
+    p = sol.make_params(1, 100, 4, 128)
+    assert _fwd_nr(sol, p, _nr(sol, **over)) == sol.SOL_ERR_INVALID_ARG
+    assert _text(sol).startswith("sol_qk_norm_rope:")
+    assert _bwd_nr(sol, p, _nr(sol, **over)) == sol.SOL_ERR_INVALID_ARG
+    assert _text(sol).startswith("sol_qk_norm_rope_bwd:")
+
+
+def test_norm_rope_refusals(sol):
+    p = sol.make_params(1, 100, 4, 128)
+    assert _fwd_nr(sol, p, None) == sol.SOL_ERR_INVALID_ARG
+    for name in ("q", "k", "qo", "ko"):
+        assert _fwd_nr(sol, p, _nr(sol), **{name: None}) == sol.SOL_ERR_INVALID_ARG and "NULL" in _text(sol)
+        assert _fwd_nr(sol, p, _nr(sol), **{name: 4104}) == sol.SOL_ERR_INVALID_ARG and "aligned" in _text(sol)
+    assert _fwd_nr(sol, sol.make_params(1, 100, 4, 128, out_strides=(51200, 0, 128)), _nr(sol)) == sol.SOL_ERR_INVALID_ARG
+    assert _fwd_nr(sol, sol.make_params(1, 100, 4, 96), _nr(sol)) == sol.SOL_ERR_UNSUPPORTED
+    assert _fwd_nr(sol, sol.make_params(1, 0, 4, 128), _nr(sol), None, None, None, None) == sol.SOL_OK
+    for name in ("q", "k", "dqo", "dko", "dq", "dk", "ws"):
+        assert _bwd_nr(sol, p, _nr(sol), **{name: None}) == sol.SOL_ERR_INVALID_ARG and "NULL" in _text(sol)
+    for name in ("q", "dqo", "dk", "dqw", "dkw"):
+        assert _bwd_nr(sol, p, _nr(sol), **{name: 4104}) == sol.SOL_ERR_INVALID_ARG and "aligned" in _text(sol)
+    assert _bwd_nr(sol, p, _nr(sol), gs=(0, 0, 128)) == sol.SOL_ERR_INVALID_ARG
+    assert _bwd_nr(sol, p, _nr(sol), ws=4096 + 64) == sol.SOL_ERR_INVALID_ARG
+    assert _bwd_nr(sol, p, _nr(sol), ws_bytes=sol.sol_qk_norm_rope_bwd_workspace_bytes(p) - 1) == sol.SOL_ERR_WORKSPACE
+    # a norm without tables or weights passes the checks and reaches the next one
+    bare = _nr(sol, q_weight=None, k_weight=None, rot_dim=0, cos=None, sin=None)
+    assert _bwd_nr(sol, p, bare, ws_bytes=1) == sol.SOL_ERR_WORKSPACE
+
+
+def test_make_norm_rope(sol):
+    w, t = torch.ones(128), torch.zeros(10, 32)
+    nr = sol.make_norm_rope(w, w, t, t.clone())
+    assert (nr.rot_dim, nr.weight_type, nr.table_stride_n, nr.table_stride_b) == (64, 0, 32, 0)
+    assert nr.tensors[0] is w
+    nr = sol.make_norm_rope(w.bfloat16(), None, torch.zeros(3, 10, 32), torch.zeros(3, 10, 32), interleaved=True)
+    assert (nr.weight_type, nr.interleaved, nr.table_stride_b, nr.k_weight) == (1, 1, 320, None)
+    assert sol.make_norm_rope(None, None).rot_dim == 0
+    for bad in (lambda: sol.make_norm_rope(w, w.bfloat16()), lambda: sol.make_norm_rope(w.double(), None),
+                lambda: sol.make_norm_rope(w, w, t), lambda: sol.make_norm_rope(w, w, t, t.double()),
+                lambda: sol.make_norm_rope(w, w, t, t[:, :16]), lambda: sol.make_norm_rope(w, w, t, t, rot_dim=32),
+                lambda: sol.make_norm_rope(w, w, t, torch.zeros(32, 10).t()), lambda: sol.make_norm_rope(w, w, rot_dim=16),
+                lambda: sol.make_norm_rope(torch.ones(256)[::2], w)):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_python_refusals(sol):
+    q = torch.zeros(1, 64, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        sol.differentiable_attention(q, q, q)           # host tensors
+    with pytest.raises(ValueError):
+        sol.qk_norm_rope(q, q, None, None)
+    p = sol.make_params(1, 64, 2, 64)
+    buf = sol.alloc_buffers(p, "cpu")
+    with pytest.raises(ValueError, match="lse"):
+        sol.backward(p, q, q, q, buf, q, sol.alloc_grads(p, "cpu"))
+
+
+def test_no_gpu_is_an_error(sol):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    p = sol.make_params(1, 100, 4, 128)
+    assert _bwd(sol, p) == sol.SOL_ERR_CUDA
+    assert _fwd_nr(sol, p, _nr(sol)) == sol.SOL_ERR_CUDA
