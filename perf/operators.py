@@ -249,7 +249,8 @@ def prepare(case, seed):
             sol.sol_pool(p, q, k, v, buf.ws)
             counts = sel.sum(-1).view(-1)
             st["row_ptr"] = torch.nn.functional.pad(counts.cumsum(0), (1, 0)).int()
-            st["col_idx"] = sel.view(-1, sel.shape[-1]).nonzero()[:, 1].int().contiguous()
+            entries = sel.view(-1, sel.shape[-1]).nonzero()[:, 1].int()
+            st["col_idx"] = torch.nn.functional.pad(entries, (0, 1))   # an address even where no block is listed
             st.update(p=p, ws=buf.ws, g=sol.alloc_grads(p, DEV))
         return st
     q, k, qw, kw, g = _rope_inputs(c, seed)
