@@ -7,6 +7,7 @@
 // link the PyTorch C++ ABI, and on an architecture mismatch stops with an
 // error naming the required and the detected compute capability, with no
 // fallback.
+#include <cuda.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -45,6 +46,25 @@ int g_arch_cc[kMaxDevices];
 int* g_status_ptr[kMaxDevices];
 std::mutex g_arch_mu;
 
+// Makes the device's primary context current on a host thread that has none yet
+// (e.g. a framework's backward thread): the runtime would do so at the first
+// launch, but the tensor maps are encoded by the driver before it.
+sol_status bind_context(int dev) {
+  typedef CUresult (*GetCurrent)(CUcontext*);
+  static GetCurrent get = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<GetCurrent>(p);
+  }();
+  CUcontext ctx = nullptr;
+  if (get && get(&ctx) == CUDA_SUCCESS && ctx) return SOL_OK;
+  const cudaError_t e = cudaSetDevice(dev);
+  return e == cudaSuccess ? SOL_OK : cuda_fail(e, "cudaSetDevice");
+}
+
 // Checks the current device once and records the device address of its
 // status word (the host name of a __device__ variable is not an address).
 sol_status check_arch(int** status = nullptr) {
@@ -71,7 +91,7 @@ sol_status check_arch(int** status = nullptr) {
     return fail(SOL_ERR_UNSUPPORTED, "libsol requires compute capability 10.0 (sm_100a, B200); device %d is %d.%d",
                 dev, g_arch_cc[dev] / 10, g_arch_cc[dev] % 10);
   if (status) *status = g_status_ptr[dev];
-  return SOL_OK;
+  return bind_context(dev);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -18,7 +18,10 @@
 //           the anchor's query rows.
 // No gradient is added atomically: the queries' pass and the keys' pass each own
 // their outputs (the logits are computed in both), so results are deterministic.
+#include <cuda.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -127,200 +130,627 @@ __global__ void __launch_bounds__(kTWarps * 32) tplan_kernel(const BwdArgs a) {
   }
 }
 
-// ---- block gradients, fp32 ---------------------------------------------------------------------------
-// The simple form of the three passes.  A CTA owns 64 rows (queries, keys or
-// centroids) and streams 64-row blocks of the other side through shared memory,
-// everything in fp32:
-//   kind 0: own = (Q, dO) of query block i; streams its listed (K, V) blocks, then
-//           the centroids; acc1 = dq / s
-//   kind 1: own = (K, V) of key block j; streams the (Q, dO) blocks that list it;
-//           acc1 = dk / s, acc2 = dv
-//   kind 2: own = 64 centroids; streams the (Q, dO) blocks of one query range;
-//           acc1 = gk / s, acc2 = gv, and gb
+// ---- the passes over block pairs ---------------------------------------------------------------------
+// Both passes run on the tensor cores with 64-row blocks of the streamed side.
+//
+//   dq_kernel    a CTA owns 128 query rows (two consecutive query blocks, M = 128)
+//                and walks the union of their lists, one 64-key block a step, then
+//                64 centroids a step: S = Q K^T, dP = dO V^T, dQ += dS K.  Q and dO
+//                sit in TMEM as A operands, so a step reads only K and V from
+//                shared memory.
+//   dkv_kernel   a CTA owns 128 key rows (two consecutive key blocks) or 128
+//                centroids and walks the query blocks that take either, one a step,
+//                transposed: S = K Q^T, dP = V dO^T, dV += P dO, dK += dS Q.  P and
+//                dS come out with their rows in TMEM lanes, as an A operand needs.
+//
+// A half of the tile that a step does not concern gets p = ds = 0 (its warps skip
+// the exponentials).  Roles (12 warps): warp 0 loads the tiles with TMA, warp 1
+// issues the MMAs, warps 4-11 are two softmax warpgroups that take alternate
+// steps, one thread per TMEM lane.  A step's S and dP live in one of two 128-column
+// TMEM stages; P and dS (bf16) are written over S.  The MMAs of step t+2 follow
+// those that read P and dS of step t in the in-order tensor pipe, so a stage
+// needs no other guard.  Every wait is bounded; on expiry the kernel raises
+// SOL_ERR_TIMEOUT, drains what it issued and frees TMEM.
+constexpr int kThreads = 384;            // 4 control warps + 2 softmax warpgroups
+constexpr int kMaxWords = kMaxKeyBlocks / 32;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void cta_sync() {
+  __syncwarp();
+  __syncthreads();
+}
+
+// Shared-memory and TMEM layout.  Streamed tiles are 64 rows in 128-byte column
+// chunks (SW128); the owned tiles of dkv_kernel are 128 rows.
 template <int D>
-struct SimtSmem {
-  float own1[64][D + 4], own2[64][D + 4], str1[64][D + 4], str2[64][D + 4];
-  float P[64][65], dS[64][65];
-  float nl[64], nd[64], add[64], gb[64];
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kSChunk = 64 * 128;            // one column chunk of a streamed tile
+  static constexpr int kSTile = 64 * D * 2;           // streamed tile
+  static constexpr int kOChunk = 128 * 128;           // one column chunk of an owned tile
+  static constexpr int kOTile = 128 * D * 2;
+  static constexpr int kDqStages = 5, kKvStages = 4;  // pairs of streamed tiles in flight
+  // TMEM columns.  dq: Q | dO | dQ | two stages; dkv: dV | dK | two stages.
+  static constexpr uint32_t kStage = 256;             // stage g: S at kStage + 128 g, dP 64 columns on
+  static constexpr uint32_t kQ = 0, kDo = 64, kDq = 128;
+  static constexpr uint32_t kDv = 0, kDk = 128;
 };
 
+struct Bars {
+  uint64_t own_full;                // owned tiles have landed (dkv: TMA) / are in TMEM (dq: softmax threads)
+  uint64_t full[5], empty[5];       // ring of streamed tile pairs
+  uint64_t s_full[2], p_full[2];    // S and dP of a step are in TMEM; P and dS are
+  uint64_t final_mma;
+};
+
+struct DqExtra {
+  Bars bar;
+  uint32_t tmem_base;
+  int abort_flag, n_union, n_cent;
+  uint32_t sel[2][kMaxWords];
+  int list[kMaxKeyBlocks];                        // union entries: j | needA << 16 | needB << 17
+  int cent[16];                                   // 64-centroid units: u | liveA << 16 | liveB << 17
+  alignas(16) float cent_add[16][2][64];          // log2-unit offsets, -inf where masked
+  alignas(16) float tail_add[64];                 // 0 for valid rows of the last key block, -inf past N
+};
+
+template <int S>
+struct KvExtra {
+  Bars bar;
+  uint32_t tmem_base;
+  int abort_flag, n_steps;
+  int list[kMaxKeyBlocks];                        // query blocks: i | needA << 16 | needB << 17
+  uint32_t cword[128][4];                         // centroids: the step's exact-block bits of this tile
+  alignas(16) float nl[S][64], nd[S][64];         // per ring stage: -lse, -delta of the query rows
+  alignas(16) float gsum[2][2][128];              // exact: the two blocks' gk, gv
+  float gb[128];
+};
+
+// TMA loads of one streamed pair (two 64-row tiles).
 template <int D>
-__device__ void load_tile(float (*dst)[D + 4], const __nv_bfloat16* src, int64_t sn, int rows) {
-  for (int e = threadIdx.x; e < 64 * D / 8; e += 256) {
-    const int r = e / (D / 8), c = e % (D / 8);
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (r < rows) u = *reinterpret_cast<const uint4*>(src + (int64_t)r * sn + 8 * c);
-    unpack8(u, &dst[r][8 * c]);
+__device__ __forceinline__ void load_pair4(uint8_t* dst, const CUtensorMap* m1, const CUtensorMap* m2, int row, int h, int b,
+                                           uint64_t* bar) {
+  for (int c = 0; c < Cfg<D>::kChunks; ++c) {
+    tma_load_4d(dst + c * Cfg<D>::kSChunk, m1, c * 64, h, row, b, bar);
+    tma_load_4d(dst + Cfg<D>::kSTile + c * Cfg<D>::kSChunk, m2, c * 64, h, row, b, bar);
   }
 }
 
-template <int D, int kind>
-__global__ void __launch_bounds__(256) simt_kernel(const BwdArgs a) {
-  extern __shared__ uint8_t raw[];
-  SimtSmem<D>& x = *reinterpret_cast<SimtSmem<D>*>(raw);
-  const int own = blockIdx.y;
-  const int64_t bh = blockIdx.x;
-  const int split = blockIdx.z;
-  const int b = (int)(bh / a.H), h = (int)(bh % a.H), tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int ntq = (a.nb + 1) / 2, mw = a.mask_words, pi = plan_ints(mw, a.nb);
-  const float sl2 = a.scale * kLog2e;
-  auto in = [&](const __nv_bfloat16* p, int n) { return p + (int64_t)b * a.sb + (int64_t)n * a.sn + (int64_t)h * a.sh; };
-  auto out = [&](const __nv_bfloat16* p, int n) { return p + (int64_t)b * a.ob + (int64_t)n * a.on + (int64_t)h * a.oh; };
-  auto grad = [&](__nv_bfloat16* p, int n) { return p + (int64_t)b * a.gb + (int64_t)n * a.gn + (int64_t)h * a.gh; };
-  auto word = [&](int i, int w) {   // exact-block bits of query block i
-    return (uint32_t)a.plan[(bh * ntq + (i >> 1)) * pi + 16 + (i & 1) * mw + w];
-  };
-  const int rows_own = min(64, a.N - 64 * own);
-  const int crows = min(64, a.nb - 64 * own);   // kind 2: centroids of this tile
-  if (kind == 0) {
-    load_tile<D>(x.own1, in(a.q, 64 * own), a.sn, rows_own);
-    load_tile<D>(x.own2, out(a.d_o, 64 * own), a.on, rows_own);
-    if (tid < 64) { x.nl[tid] = a.nlse[bh * 64 * a.nb + 64 * own + tid]; x.nd[tid] = a.ndelta[bh * 64 * a.nb + 64 * own + tid]; }
-  } else if (kind == 1) {
-    load_tile<D>(x.own1, in(a.k, 64 * own), a.sn, rows_own);
-    load_tile<D>(x.own2, in(a.v, 64 * own), a.sn, rows_own);
-  } else {
-    load_tile<D>(x.own1, a.kbar16 + (bh * a.nb + 64 * own) * D, D, crows);
-    load_tile<D>(x.own2, a.vbar16 + (bh * a.nb + 64 * own) * D, D, crows);
-    if (tid < 64) { x.add[tid] = tid < crows ? a.cbias[bh * a.nb + 64 * own + tid] * kLog2e : -INFINITY; x.gb[tid] = 0.f; }
-  }
-  float acc1[4][D / 16], acc2[4][D / 16];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) acc1[i][j] = acc2[i][j] = 0.f;
+// Streamed-tile descriptors: as B operand with the head dims as K (K-major), and
+// with the rows as K (MN-major).
+template <int D>
+__device__ __forceinline__ uint64_t kmaj(uint64_t base, int kk, int chunk) {
+  return base + (uint64_t)(((kk >> 2) * chunk + (kk & 3) * 32) >> 4);
+}
 
-  const int ctiles = kind == 0 && a.centroids ? (a.nb + 63) / 64 : 0;
-  const int lo = kind == 2 ? (int)((int64_t)a.nb * split / a.splits) : 0;
-  const int hi = kind == 2 ? (int)((int64_t)a.nb * (split + 1) / a.splits) : a.nb + ctiles;
-  const int* tp = a.tplan + (bh * ntq + (own >> 1)) * tplan_ints(a.nb);
-  const int steps = kind == 1 ? tp[0] : hi;
-  for (int t = lo; t < steps; ++t) {
-    int blk = t;
-    bool cent = false;
-    if (kind == 0) {
-      cent = t >= a.nb;
-      if (!cent && !((word(own, t >> 5) >> (t & 31)) & 1u)) continue;
-      if (cent) blk = t - a.nb;
-    } else if (kind == 1) {
-      const int e = tp[16 + t];
-      if (!((e >> (16 + (own & 1))) & 1)) continue;
-      blk = e & 0xffff;
-    }
-    __syncthreads();
-    if (kind == 0 && !cent) {
-      load_tile<D>(x.str1, in(a.k, 64 * blk), a.sn, min(64, a.N - 64 * blk));
-      load_tile<D>(x.str2, in(a.v, 64 * blk), a.sn, min(64, a.N - 64 * blk));
-      if (tid < 64) x.add[tid] = 64 * blk + tid < a.N ? 0.f : -INFINITY;
-    } else if (kind == 0) {
-      const int cr = min(64, a.nb - 64 * blk);
-      load_tile<D>(x.str1, a.kbar16 + (bh * a.nb + 64 * blk) * D, D, cr);
-      load_tile<D>(x.str2, a.vbar16 + (bh * a.nb + 64 * blk) * D, D, cr);
-      if (tid < 64) {
-        const bool live = tid < cr && !((word(own, 2 * blk + (tid >> 5)) >> (tid & 31)) & 1u);
-        x.add[tid] = live ? a.cbias[bh * a.nb + 64 * blk + tid] * kLog2e : -INFINITY;
-      }
-    } else {
-      load_tile<D>(x.str1, in(a.q, 64 * blk), a.sn, min(64, a.N - 64 * blk));
-      load_tile<D>(x.str2, out(a.d_o, 64 * blk), a.on, min(64, a.N - 64 * blk));
-      if (tid < 64) { x.nl[tid] = a.nlse[bh * 64 * a.nb + 64 * blk + tid]; x.nd[tid] = a.ndelta[bh * 64 * a.nb + 64 * blk + tid]; }
-    }
-    __syncthreads();
-    float S[4][4], dP[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) S[i][j] = dP[i][j] = 0.f;
-    for (int d = 0; d < D; ++d) {
-      float u[4], w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = x.own1[4 * ty + i][d];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = x.str1[tx + 16 * j][d];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[i][j] = fmaf(u[i], w[j], S[i][j]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = x.own2[4 * ty + i][d];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = x.str2[tx + 16 * j][d];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dP[i][j] = fmaf(u[i], w[j], dP[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * ty + i, c = tx + 16 * j;
-        float e = S[i][j] * sl2, nd;
-        if (kind == 0) { e += x.add[c] + x.nl[r]; nd = x.nd[r]; }
-        else { e += x.nl[c]; nd = x.nd[c]; }
-        if (kind == 2) {
-          const bool live = r < crows && !((word(blk, 2 * own + (r >> 5)) >> (r & 31)) & 1u);
-          e = live ? e + x.add[r] : -INFINITY;
-        }
-        const float p = exp2f(e);
-        x.P[r][c] = p;
-        x.dS[r][c] = p * (dP[i][j] + nd);
-      }
-    __syncthreads();
-    if (kind == 2 && tid < 64) {
-      float s = 0.f;
-      for (int c = 0; c < 64; ++c) s += x.dS[tid][c];
-      x.gb[tid] += s;
-    }
-    for (int c = 0; c < 64; ++c) {
-      float w1[D / 16], w2[D / 16];
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) { w1[j] = x.str1[c][tx + 16 * j]; if (kind != 0) w2[j] = x.str2[c][tx + 16 * j]; }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ds = x.dS[4 * ty + i][c], p = x.P[4 * ty + i][c];
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          acc1[i][j] = fmaf(ds, w1[j], acc1[i][j]);
-          if (kind != 0) acc2[i][j] = fmaf(p, w2[j], acc2[i][j]);
-        }
-      }
-    }
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+          const __grid_constant__ CUtensorMap mkb, const __grid_constant__ CUtensorMap mvb, const BwdArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DqExtra& x = *reinterpret_cast<DqExtra*>(ring + C::kDqStages * 2 * C::kSTile);
+  Bars& bar = x.bar;
+  volatile int* abort_flag = &x.abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ntq = (a.nb + 1) / 2, mw = a.mask_words;
+  const int tq = blockIdx.x % ntq;
+  const int64_t bh = blockIdx.x / ntq;
+  const int b = (int)(bh / a.H), h = (int)(bh % a.H), i0 = 2 * tq;
+
+  if (tid == 0) {
+    mbar_init(&bar.own_full, 256);
+    for (int s = 0; s < C::kDqStages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&bar.s_full[s], 1); mbar_init(&bar.p_full[s], 4); }
+    mbar_init(&bar.final_mma, 1);
+    x.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncthreads();
-  const int64_t bhs = (int64_t)a.B * a.H;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i, n = 64 * own + r;
-    for (int j = 0; j < D / 16; ++j) {
-      const int d = tx + 16 * j;
-      float y1 = a.scale * acc1[i][j], y2 = acc2[i][j];
-      if (kind == 0 && n < a.N) {
-        if (a.da && (n >= a.prefix || a.prefix == a.N)) y1 += a.da[bh * D + d];
-        grad(a.dq, n)[d] = __float2bfloat16(y1);
-      } else if (kind == 1 && n < a.N) {
-        if (a.centroids) {
-          float gk = 0.f, gv = 0.f;
-          for (int s = 0; s < a.splits; ++s) {
-            gk += a.gk[((s * bhs + bh) * a.nb + own) * D + d];
-            gv += a.gv[((s * bhs + bh) * a.nb + own) * D + d];
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&x.tmem_base)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  const int n_tail = a.N - 64 * (a.nb - 1);
+  if (tid < 64) x.tail_add[tid] = tid < n_tail ? 0.f : -INFINITY;
+  {
+    const int* P = a.plan + (bh * ntq + tq) * plan_ints(mw, a.nb);
+    for (int e = tid; e < 2 * mw + a.nb; e += kThreads) {
+      const int v = P[16 + e];
+      if (e >= 2 * mw) x.list[e - 2 * mw] = v;
+      else x.sel[e / mw][e % mw] = (uint32_t)v;
+    }
+    if (tid == 0) x.n_union = P[0];
+  }
+  cta_sync();
+  if (warp == 0) {   // 64-centroid units that either query block leaves to its centroids
+    const int units = a.centroids ? (a.nb + 63) / 64 : 0;
+    bool l0 = false, l1 = false;
+    if (lane < units) {
+      for (int w = 2 * lane; w < 2 * lane + 2 && w < mw; ++w) {
+        const uint32_t vm = a.nb - 32 * w >= 32 ? 0xffffffffu : (1u << (a.nb - 32 * w)) - 1u;
+        l0 |= (~x.sel[0][w] & vm) != 0u;
+        l1 |= i0 + 1 < a.nb && (~x.sel[1][w] & vm) != 0u;
+      }
+    }
+    const uint32_t any = __ballot_sync(0xffffffffu, l0 || l1);
+    if (l0 || l1) x.cent[__popc(any & ((1u << lane) - 1u))] = lane | (int)l0 << 16 | (int)l1 << 17;
+    if (lane == 0) x.n_cent = __popc(any);
+  }
+  cta_sync();
+  for (int e = tid; e < 128 * x.n_cent; e += kThreads) {
+    const int slot = e >> 7, hf = (e >> 6) & 1, c = e & 63, j = 64 * (x.cent[slot] & 0xffff) + c;
+    const bool live = j < a.nb && i0 + hf < a.nb && !((x.sel[hf][j >> 5] >> (j & 31)) & 1u);
+    x.cent_add[slot][hf][c] = live ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
+  }
+  fence_before();
+  cta_sync();
+  fence_after();
+  const uint32_t tmem = x.tmem_base;
+  const int T = x.n_union + x.n_cent;
+
+  if (warp == 0) {
+    if (lane == 0) {   // K and V (centroid) tiles
+      int nl = 0;
+      for (int t = 0; t < T; ++t) {
+        const int s = t % C::kDqStages, n = t / C::kDqStages;
+        if (!wait_bar(&bar.empty[s], (n & 1) ^ 1, abort_flag, a.status)) break;
+        uint8_t* dst = ring + s * 2 * C::kSTile;
+        ++nl;
+        mbar_expect_tx(&bar.full[s], 2 * C::kSTile);
+        if (t < x.n_union) {
+          load_pair4<D>(dst, &mk, &mv, 64 * (x.list[t] & 0xffff), h, b, &bar.full[s]);
+        } else {
+          const int row = 64 * (x.cent[t - x.n_union] & 0xffff);
+          for (int c = 0; c < C::kChunks; ++c) {
+            tma_load_3d(dst + c * C::kSChunk, &mkb, c * 64, row, (int)bh, &bar.full[s]);
+            tma_load_3d(dst + C::kSTile + c * C::kSChunk, &mvb, c * 64, row, (int)bh, &bar.full[s]);
           }
-          const int64_t at = bh * 64 * a.nb + n, plane = bhs * 64 * a.nb;
-          const float al = a.mode ? a.coef[at] : 1.f / rows_own, ga = a.mode ? a.coef[2 * plane + at] : al;
-          y1 += al * gk;
-          y2 += ga * gv;
-          if (a.mode) y1 += a.coef[plane + at] * a.anchor[bh * D + d];
         }
-        grad(a.dk, n)[d] = __float2bfloat16(y1);
-        grad(a.dv, n)[d] = __float2bfloat16(y2);
-      } else if (kind == 2 && r < crows) {
-        const int64_t at = ((split * bhs + bh) * a.nb + n) * D + d;
-        a.gk[at] = y1;
-        a.gv[at] = y2;
+      }
+      for (int s = 0; s < C::kDqStages; ++s) {   // every armed load has landed before the CTA may exit
+        const int cnt = (nl + C::kDqStages - 1 - s) / C::kDqStages;
+        if (cnt) drain_bar(&bar.full[s], (cnt - 1) & 1, a.status);
+      }
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
+    const uint64_t sd0 = sdesc(smem_u32(ring), 16, 1024), gd0 = sdesc(smem_u32(ring), C::kSChunk, 1024);
+    auto stage_off = [&](int t) { return (uint64_t)((t % C::kDqStages) * 2 * (C::kSTile >> 4)); };
+    auto products = [&](int t) {   // S(t), dP(t)
+      const uint32_t st = tmem + C::kStage + 128 * (t & 1);
+      const uint64_t kd = sd0 + stage_off(t), vd = kd + (C::kSTile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ts_w(st, tmem + C::kQ + kk * 8, kmaj<D>(kd, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ts_w(st + 64, tmem + C::kDo + kk * 8, kmaj<D>(vd, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+      mma_commit_w(&bar.s_full[t & 1]);
+    };
+    auto wait_kv = [&](int t) {
+      return __all_sync(0xffffffffu, wait_bar(&bar.full[t % C::kDqStages], (t / C::kDqStages) & 1, abort_flag, a.status));
+    };
+    bool ok = T == 0 || __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
+    fence_after();
+    for (int t = 0; t < 2 && t < T && ok; ++t)
+      if ((ok = wait_kv(t))) products(t);
+    for (int t = 0; t < T && ok; ++t) {
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.p_full[t & 1], (t >> 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      fence_after();
+      const uint32_t ds = tmem + C::kStage + 128 * (t & 1);
+      const uint64_t kd = gd0 + stage_off(t);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ts_w(tmem + C::kDq, ds + kk * 8, kd + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
+      mma_commit_w(&bar.empty[t % C::kDqStages]);
+      if (t + 2 < T) {
+        if (!(ok = wait_kv(t + 2))) break;
+        products(t + 2);
+      }
+    }
+    mma_commit_w(&bar.final_mma);
+    drain_bar(&bar.final_mma, 0, a.status);
+  } else if (warp >= 4) {
+    const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
+    const int row = 64 * i0 + r;
+    const bool valid = row < a.N;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
+    {   // group 0 puts Q, group 1 dO into TMEM (rows past N as zeros)
+      const __nv_bfloat16* src = g == 0 ? a.q + (int64_t)b * a.sb + (int64_t)row * a.sn + (int64_t)h * a.sh
+                                        : a.d_o + (int64_t)b * a.ob + (int64_t)row * a.on + (int64_t)h * a.oh;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (valid) v = reinterpret_cast<const uint4*>(src + 64 * c)[u];
+          w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
+        }
+        tmem_st32(lane_addr + (g == 0 ? C::kQ : C::kDo) + 32 * c, w);
+      }
+      tmem_wait_st();
+      fence_before();
+      mbar_arrive(&bar.own_full);
+    }
+    const bool in_range = i0 + hf < a.nb;
+    const float nl = in_range ? a.nlse[bh * 64 * a.nb + row] : -INFINITY;
+    const float nd = in_range ? a.ndelta[bh * 64 * a.nb + row] : 0.f;
+    const float sl2 = a.scale * kLog2e;
+    const uint64_t sl22 = f2pack(sl2, sl2), nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
+    bool ok = true;
+    for (int t = g; t < T && ok; t += 2) {
+      bool need;
+      const float* add = nullptr;
+      if (t < x.n_union) {
+        const int e = x.list[t];
+        need = (e >> (16 + hf)) & 1;
+        if ((e & 0xffff) == a.nb - 1) add = x.tail_add;
+      } else {
+        need = (x.cent[t - x.n_union] >> (16 + hf)) & 1;
+        add = x.cent_add[t - x.n_union][hf];
+      }
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.s_full[g], (t >> 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      fence_after();
+      const uint32_t st = lane_addr + C::kStage + 128 * g;
+      uint32_t pk[32];
+      if (need) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float s[32], dp[32];
+          tmem_ld32(st + 32 * hh, s);
+          tmem_ld32(st + 64 + 32 * hh, dp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            uint64_t e2 = ffma2(f2pack(s[2 * c], s[2 * c + 1]), sl22, nl2);
+            if (add) {
+              const float2 o = reinterpret_cast<const float2*>(add)[16 * hh + c];
+              e2 = fadd2(e2, f2pack(o.x, o.y));
+            }
+            float e0, e1, d0, d1;
+            f2unpack(e2, e0, e1);
+            const uint64_t p2 = f2pack(ex2(e0), ex2(e1));
+            f2unpack(fmul2(p2, fadd2(f2pack(dp[2 * c], dp[2 * c + 1]), nd2)), d0, d1);
+            pk[16 * hh + c] = pack_bf16(d0, d1);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = 0u;
+      }
+      tmem_st32(st, pk);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[g]);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
+    if (ok && !*abort_flag) {
+      fence_after();
+      const bool anch = a.da && (row >= a.prefix || a.prefix == a.N);
+      __nv_bfloat16* dst = a.dq + (int64_t)b * a.gb + (int64_t)row * a.gn + (int64_t)h * a.gh;
+      const float* da = a.da + bh * D;
+      for (int c = g; c < D / 32; c += 2) {
+        float v[32];
+        __syncwarp();
+        tmem_ld32(lane_addr + C::kDq + 32 * c, v);
+        tmem_wait_ld();
+        if (!valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] = T > 0 ? a.scale * v[e] : 0.f;
+          if (anch) v[e] += da[32 * c + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4*>(dst + 32 * c + e) =
+              make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
+                         pack_bf16(v[e + 6], v[e + 7]));
       }
     }
   }
-  if (kind == 2 && tid < crows) a.gb_[(split * bhs + bh) * a.nb + 64 * own + tid] = x.gb[tid];
+  fence_before();
+  cta_sync();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
+  }
+}
+
+template <int D, bool kCent>
+__global__ void __launch_bounds__(kThreads, 1)
+dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo,
+           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdArgs a) {
+  using C = Cfg<D>;
+  constexpr int S = C::kKvStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* own = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = own + 2 * C::kOTile;
+  KvExtra<S>& x = *reinterpret_cast<KvExtra<S>*>(ring + S * 2 * C::kSTile);
+  Bars& bar = x.bar;
+  volatile int* abort_flag = &x.abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ntq = (a.nb + 1) / 2, mw = a.mask_words;
+  const int tiles = kCent ? (a.nb + 127) / 128 : ntq;
+  const int tk = blockIdx.x % tiles;
+  const int64_t bh = (blockIdx.x / tiles) % ((int64_t)a.B * a.H), bhs = (int64_t)a.B * a.H;
+  const int split = kCent ? (int)(blockIdx.x / tiles / bhs) : 0;
+  const int b = (int)(bh / a.H), h = (int)(bh % a.H);
+
+  if (tid == 0) {
+    mbar_init(&bar.own_full, 1);
+    for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&bar.s_full[s], 1); mbar_init(&bar.p_full[s], 4); }
+    mbar_init(&bar.final_mma, 1);
+    x.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_expect_tx(&bar.own_full, 2 * C::kOTile);
+    for (int c = 0; c < C::kChunks; ++c) {
+      uint8_t* dk = own + c * C::kOChunk;
+      uint8_t* dv = dk + C::kOTile;
+      if (kCent) {
+        for (int hf = 0; hf < 2; ++hf) {
+          tma_load_3d(dk + hf * (C::kOChunk / 2), &mk, c * 64, 128 * tk + 64 * hf, (int)bh, &bar.own_full);
+          tma_load_3d(dv + hf * (C::kOChunk / 2), &mv, c * 64, 128 * tk + 64 * hf, (int)bh, &bar.own_full);
+        }
+      } else {
+        for (int hf = 0; hf < 2; ++hf) {
+          tma_load_4d(dk + hf * (C::kOChunk / 2), &mk, c * 64, h, 128 * tk + 64 * hf, b, &bar.own_full);
+          tma_load_4d(dv + hf * (C::kOChunk / 2), &mv, c * 64, h, 128 * tk + 64 * hf, b, &bar.own_full);
+        }
+      }
+    }
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&x.tmem_base)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (kCent) {
+    // the range's query blocks that leave any of the tile's key blocks to its centroid
+    const int lo = (int)((int64_t)a.nb * split / a.splits), hi = (int)((int64_t)a.nb * (split + 1) / a.splits);
+    if (warp == 2) {
+      int n = 0;
+      for (int i = lo; i < hi; i += 32) {
+        uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (i + lane < hi) {
+          const int* P = a.plan + (bh * ntq + ((i + lane) >> 1)) * plan_ints(mw, a.nb) + 16 + ((i + lane) & 1) * mw;
+          for (int e = 0; e < 4; ++e) {
+            const int base = 128 * tk + 32 * e;
+            if (base >= a.nb) continue;
+            w[e] = (uint32_t)P[4 * tk + e];
+            if (a.nb - base < 32) w[e] |= ~((1u << (a.nb - base)) - 1u);
+          }
+        }
+        const bool live = (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu;
+        const uint32_t any = __ballot_sync(0xffffffffu, live);
+        if (live) {
+          const int at = n + __popc(any & ((1u << lane) - 1u));
+          x.list[at] = i + lane;
+          for (int e = 0; e < 4; ++e) x.cword[at][e] = w[e];
+        }
+        n += __popc(any);
+      }
+      if (lane == 0) x.n_steps = n;
+    }
+  } else {
+    const int* P = a.tplan + (bh * ntq + tk) * tplan_ints(a.nb);
+    for (int e = tid; e < a.nb; e += kThreads) x.list[e] = P[16 + e];
+    if (tid == 0) x.n_steps = P[0];
+  }
+  fence_before();
+  cta_sync();
+  fence_after();
+  const uint32_t tmem = x.tmem_base;
+  const int T = x.n_steps;
+
+  if (warp == 0) {
+    if (lane == 0) {   // Q and dO tiles, -lse and -delta of their rows
+      int nl = 0;
+      for (int t = 0; t < T; ++t) {
+        const int s = t % S, n = t / S, i = x.list[t] & 0xffff;
+        if (!wait_bar(&bar.empty[s], (n & 1) ^ 1, abort_flag, a.status)) break;
+        ++nl;
+        mbar_expect_tx(&bar.full[s], 2 * C::kSTile + 512);
+        load_pair4<D>(ring + s * 2 * C::kSTile, &mq, &mdo, 64 * i, h, b, &bar.full[s]);
+        bulk_load(x.nl[s], a.nlse + (bh * a.nb + i) * 64, 256, &bar.full[s]);
+        bulk_load(x.nd[s], a.ndelta + (bh * a.nb + i) * 64, 256, &bar.full[s]);
+      }
+      for (int s = 0; s < S; ++s) {
+        const int cnt = (nl + S - 1 - s) / S;
+        if (cnt) drain_bar(&bar.full[s], (cnt - 1) & 1, a.status);
+      }
+      drain_bar(&bar.own_full, 0, a.status);
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
+    const uint64_t kd = sdesc(smem_u32(own), 16, 1024), vd = kd + (C::kOTile >> 4);
+    const uint64_t sd0 = sdesc(smem_u32(ring), 16, 1024), gd0 = sdesc(smem_u32(ring), C::kSChunk, 1024);
+    auto stage_off = [&](int t) { return (uint64_t)((t % S) * 2 * (C::kSTile >> 4)); };
+    auto products = [&](int t) {
+      const uint32_t st = tmem + C::kStage + 128 * (t & 1);
+      const uint64_t qd = sd0 + stage_off(t), od = qd + (C::kSTile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss_w(st, kmaj<D>(kd, kk, C::kOChunk), kmaj<D>(qd, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss_w(st + 64, kmaj<D>(vd, kk, C::kOChunk), kmaj<D>(od, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+      mma_commit_w(&bar.s_full[t & 1]);
+    };
+    auto wait_ring = [&](int t) {
+      return __all_sync(0xffffffffu, wait_bar(&bar.full[t % S], (t / S) & 1, abort_flag, a.status));
+    };
+    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
+    for (int t = 0; t < 2 && t < T && ok; ++t)
+      if ((ok = wait_ring(t))) products(t);
+    for (int t = 0; t < T && ok; ++t) {
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.p_full[t & 1], (t >> 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      fence_after();
+      const uint32_t st = tmem + C::kStage + 128 * (t & 1);
+      const uint64_t qd = gd0 + stage_off(t), od = qd + (C::kSTile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ts_w(tmem + C::kDv, st + kk * 8, od + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ts_w(tmem + C::kDk, st + 32 + kk * 8, qd + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
+      mma_commit_w(&bar.empty[t % S]);
+      if (t + 2 < T) {
+        if (!(ok = wait_ring(t + 2))) break;
+        products(t + 2);
+      }
+    }
+    mma_commit_w(&bar.final_mma);
+    drain_bar(&bar.final_mma, 0, a.status);
+  } else if (warp >= 4) {
+    const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
+    const float sl2 = a.scale * kLog2e;
+    const uint64_t sl22 = f2pack(sl2, sl2);
+    const int j = kCent ? 128 * tk + r : 2 * tk + hf;   // this row's centroid / key block
+    const float cadd = kCent && j < a.nb ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
+    if (!kCent && a.centroids) {   // the two blocks' centroid gradients, summed over the query ranges in order
+      for (int e = tid - 128; e < 4 * D; e += 256) {
+        const int d = e % D, half = (e / D) & 1, which = e / (2 * D), jj = 2 * tk + half;
+        const float* src = which ? a.gv : a.gk;
+        float v = 0.f;
+        if (jj < a.nb)
+          for (int s = 0; s < a.splits; ++s) v += src[((s * bhs + bh) * a.nb + jj) * D + d];
+        x.gsum[which][half][d] = v;
+      }
+    }
+    float gbs = 0.f;
+    bool ok = true;
+    for (int t = g; t < T && ok; t += 2) {
+      const int rs = t % S;
+      bool need = true;
+      uint64_t add2 = 0ull;
+      if (kCent) {
+        const float v = (x.cword[t][sub] >> lane) & 1u ? -INFINITY : cadd;
+        add2 = f2pack(v, v);
+      } else {
+        need = (x.list[t] >> (16 + hf)) & 1;
+      }
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.full[rs], (t / S) & 1, abort_flag, a.status) &&
+                                       wait_bar(&bar.s_full[g], (t >> 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      fence_after();
+      const uint32_t st = lane_addr + C::kStage + 128 * g;
+      uint32_t pp[32], pd[32];
+      if (need) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float s[32], dp[32];
+          tmem_ld32(st + 32 * hh, s);
+          tmem_ld32(st + 64 + 32 * hh, dp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 l4 = reinterpret_cast<const float4*>(x.nl[rs])[8 * hh + c];
+            const float4 d4 = reinterpret_cast<const float4*>(x.nd[rs])[8 * hh + c];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint64_t l2 = u ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y);
+              const uint64_t n2 = u ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y);
+              if (kCent) l2 = fadd2(l2, add2);
+              const int k = 4 * c + 2 * u;
+              float e0, e1, d0, d1;
+              f2unpack(ffma2(f2pack(s[k], s[k + 1]), sl22, l2), e0, e1);
+              const float p0 = ex2(e0), p1 = ex2(e1);
+              f2unpack(fmul2(f2pack(p0, p1), fadd2(f2pack(dp[k], dp[k + 1]), n2)), d0, d1);
+              if (kCent) gbs += d0 + d1;
+              pp[16 * hh + 2 * c + u] = pack_bf16(p0, p1);
+              pd[16 * hh + 2 * c + u] = pack_bf16(d0, d1);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pp[c] = pd[c] = 0u;
+      }
+      tmem_st32(st, pp);
+      tmem_st32(st + 32, pd);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[g]);
+    }
+    if (kCent && g == 0) x.gb[r] = gbs;
+    if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
+    __syncwarp();
+    bar_sync(1, 256);
+    if (ok && !*abort_flag) {
+      fence_after();
+      if (kCent) {
+        const bool store = j < a.nb;
+        const int64_t at = (split * bhs + bh) * a.nb + j;
+        if (g == 1 && store) a.gb_[at] = x.gb[r] + gbs;
+        float* dst = (g ? a.gv : a.gk) + at * D;   // group 0 stores gk, group 1 gv
+        const float mul = T > 0 ? (g ? 1.f : a.scale) : 0.f;
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          __syncwarp();
+          tmem_ld32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, v);
+          tmem_wait_ld();
+          if (!store) continue;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + 32 * c + e) =
+                T > 0 ? make_float4(mul * v[e], mul * v[e + 1], mul * v[e + 2], mul * v[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      } else {
+        const int row = 128 * tk + r;
+        const bool store = row < a.N;
+        const int64_t plane = bhs * 64 * a.nb, cr = bh * 64 * a.nb + row;
+        float mul = 0.f, beta = 0.f;   // the row's share of its centroid's gradient, and of the anchor's
+        if (store && a.centroids) {
+          mul = a.mode ? a.coef[(g ? 2 : 0) * plane + cr] : 1.f / (float)min(64, a.N - 64 * j);
+          if (a.mode && g == 0) beta = a.coef[plane + cr];
+        }
+        const float* an = a.anchor + bh * D;
+        const float* gs = x.gsum[g][hf];
+        __nv_bfloat16* dst = (g ? a.dv : a.dk) + (int64_t)b * a.gb + (int64_t)row * a.gn + (int64_t)h * a.gh;
+        const float sc = g ? 1.f : a.scale;
+        for (int c = 0; c < D / 32; ++c) {   // group 0 stores dk, group 1 dv
+          float v[32];
+          __syncwarp();
+          tmem_ld32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, v);
+          tmem_wait_ld();
+          if (!store) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            v[e] = T > 0 ? sc * v[e] : 0.f;
+            if (a.centroids) v[e] = fmaf(mul, gs[32 * c + e], v[e]);
+            if (a.centroids && a.mode && g == 0) v[e] = fmaf(beta, an[32 * c + e], v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(dst + 32 * c + e) =
+                make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
+                           pack_bf16(v[e + 6], v[e + 7]));
+        }
+      }
+    }
+  }
+  fence_before();
+  cta_sync();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
+  }
 }
 
 // ---- the pooling's gradient (modes 1, 2) -----------------------------------------------------------------
@@ -442,36 +872,77 @@ __global__ void __launch_bounds__(1024) anchor_bwd_kernel(const BwdArgs a) {
   }
 }
 
-template <int D, int kind>
-cudaError_t launch_simt(const BwdArgs& a, cudaStream_t st) {
-  const int smem = (int)sizeof(SimtSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(simt_kernel<D, kind>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(a.B * a.H, kind == 2 ? (a.nb + 63) / 64 : a.nb, kind == 2 ? a.splits : 1);
-  simt_kernel<D, kind><<<grid, 256, smem, st>>>(a);
-  return cudaGetLastError();
+template <int D>
+constexpr size_t dq_smem() { return 1024 + Cfg<D>::kDqStages * 2 * Cfg<D>::kSTile + sizeof(DqExtra); }
+template <int D>
+constexpr size_t dkv_smem() {
+  return 1024 + 2 * Cfg<D>::kOTile + Cfg<D>::kKvStages * 2 * Cfg<D>::kSTile + sizeof(KvExtra<Cfg<D>::kKvStages>);
+}
+static_assert(dq_smem<128>() <= 232448 && dkv_smem<128>() <= 232448, "shared memory");
+
+// Once per device (so that launches stay free of attribute calls, e.g. inside a
+// stream capture): opt in to the shared memory.
+template <int D>
+cudaError_t prepare() {
+  static std::atomic<int> done[64];   // zero-initialised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
+  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(dq_kernel<D>, at, (int)dq_smem<D>())) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(dkv_kernel<D, false>, at, (int)dkv_smem<D>())) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(dkv_kernel<D, true>, at, (int)dkv_smem<D>())) != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// 64-row boxes of a BTHD tensor (strides in elements) and of the [BH, nb, D] centroids.
+bool map_rows(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D, int64_t sb, int64_t sn, int64_t sh) {
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.N, (cuuint64_t)a.B};
+  const cuuint64_t str[3] = {(cuuint64_t)(a.H > 1 ? sh : D) * 2, (cuuint64_t)(a.N > 1 ? sn : D) * 2,
+                             (cuuint64_t)(a.B > 1 ? sb : D) * 2};
+  const cuuint32_t box[4] = {64, 1, 64, 1};
+  return make_map(m, p, 4, dims, str, box, kSw128);
+}
+bool map_cent(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.nb, (cuuint64_t)a.B * a.H};
+  const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.nb * D * 2};
+  const cuuint32_t box[3] = {64, 64, 1};
+  return make_map(m, p, 3, dims, str, box, kSw128);
 }
 
 template <int D>
 cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
-  stat_kernel<D><<<(unsigned)(a.B * a.nb) * ((a.H + kStatHeads - 1) / kStatHeads), 256, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  CUtensorMap mq, mk, mv, mdo, mkb, mvb;
+  if (!map_rows(&mq, a.q, a, D, a.sb, a.sn, a.sh) || !map_rows(&mk, a.k, a, D, a.sb, a.sn, a.sh) ||
+      !map_rows(&mv, a.v, a, D, a.sb, a.sn, a.sh) || !map_rows(&mdo, a.d_o, a, D, a.ob, a.on, a.oh) ||
+      !map_cent(&mkb, a.kbar16, a, D) || !map_cent(&mvb, a.vbar16, a, D))
+    return cudaErrorInvalidValue;
+  cudaError_t e = prepare<D>();
   if (e != cudaSuccess) return e;
+  stat_kernel<D><<<(unsigned)(a.B * a.nb) * ((a.H + kStatHeads - 1) / kStatHeads), 256, 0, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   AttnArgs pa{};
   pa.row_ptr = a.row_ptr; pa.col_idx = a.col_idx; pa.plan = a.plan; pa.status = a.status;
   pa.B = a.B; pa.H = a.H; pa.N = a.N; pa.nqb = pa.nkb = a.nb; pa.centroids = a.centroids;
   if ((e = launch_plan(pa, st)) != cudaSuccess) return e;
   tplan_kernel<<<dim3(a.B * a.H, a.mask_words), kTWarps * 32, 0, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.centroids && (e = launch_simt<D, 2>(a, st)) != cudaSuccess) return e;
+  const unsigned bh = (unsigned)(a.B * a.H), tiles = bh * ((a.nb + 1) / 2);
+  if (a.centroids) {
+    dkv_kernel<D, true><<<bh * ((a.nb + 127) / 128) * a.splits, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mkb, mvb, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   if (a.centroids && a.mode) {
     pool_bwd_kernel<D><<<dim3(a.B * a.H, a.nb), 256, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     anchor_bwd_kernel<D><<<a.B * a.H, 1024, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = launch_simt<D, 0>(a, st)) != cudaSuccess) return e;
-  return launch_simt<D, 1>(a, st);
+  dq_kernel<D><<<tiles, kThreads, dq_smem<D>(), st>>>(mk, mv, mkb, mvb, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  dkv_kernel<D, false><<<tiles, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mk, mv, a);
+  return cudaGetLastError();
 }
 
 }  // namespace

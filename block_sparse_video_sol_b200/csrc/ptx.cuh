@@ -117,6 +117,11 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // ---- tcgen05 (5th-generation tensor cores, TMEM accumulators) ----------------------------------
 // Shared-memory matrix descriptor, 128-byte swizzle (canonical SW128 layout:
 // 128-byte rows, 8-row groups 1024 bytes apart).

@@ -327,6 +327,54 @@ def test_zero_rows_are_finite(sol):
     assert (o == 0).all() and torch.isfinite(dq.float()).all()
 
 
+def test_calls_from_host_threads_without_a_context(sol):
+    """A thread's first CUDA call is the library's: forward and backward, each from a thread of its own."""
+    import threading
+    q, k, v, do = inputs(1, 300, 2, 128, 8)
+    p = sol.make_params(1, 300, 2, 128)
+    buf, g = sol.alloc_buffers(p, "cuda", with_lse=True), sol.alloc_grads(p, "cuda")
+    sol.forward(p, q, k, v, buf)
+    sol.backward(p, q, k, v, buf, do, g)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (buf.o, g.dq, g.dk, g.dv)]
+    for t in (buf.o, g.dq, g.dk, g.dv):
+        t.zero_()
+    stream, errors = torch.cuda.current_stream(), []
+    torch.cuda.synchronize()
+
+    def call(fn, *a):
+        try:
+            fn(*a, stream=stream)
+        except Exception as e:   # reported by the main thread
+            errors.append(e)
+
+    for a in ((sol.sol_attn_fwd, p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse),
+              (sol.backward, p, q, k, v, buf, do, g)):
+        t = threading.Thread(target=call, args=a)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert all(torch.equal(a, b) for a, b in zip(want, (buf.o, g.dq, g.dk, g.dv)))
+
+
+def test_expanded_output_gradient(sol):
+    """d_o with zero strides (one row for every position and head)."""
+    p, buf, (q, k, v, _), g = run(sol, 2, 150, 2, 128, tau=0.5)
+    row = torch.randn(128, device="cuda").bfloat16()
+    dense = row.expand(2, 150, 2, 128).contiguous()
+    want = [t.clone() for t in (sol.backward(p, q, k, v, buf, dense, g).dq, g.dk, g.dv)]
+    pe = sol.make_params(2, 150, 2, 128, tau=0.5, out_strides=(0, 0, 0))
+    # o has its own strides in this call, so it is given as an expanded row too: delta changes with it
+    zero = torch.zeros(128, device="cuda").bfloat16()
+    sol.sol_attn_bwd(pe, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, zero, buf.lse, row, g.dq, g.dk, g.dv, g.ws)
+    a = [t.clone() for t in (g.dq, g.dk, g.dv)]
+    sol.sol_attn_bwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, torch.zeros_like(q), buf.lse, dense, g.dq, g.dk, g.dv, g.ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, (g.dq, g.dk, g.dv)))
+    assert torch.equal(want[2], g.dv)
+
+
 # ---- together ---------------------------------------------------------------------------------------
 def layer(sol, qkv, w, cos, sin, **kw):
     q, k, v = qkv.unbind(2)
