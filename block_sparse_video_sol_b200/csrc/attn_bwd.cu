@@ -144,12 +144,16 @@ __global__ void __launch_bounds__(kTWarps * 32) tplan_kernel(const BwdArgs a) {
 //                dS come out with their rows in TMEM lanes, as an A operand needs.
 //
 // A half of the tile that a step does not concern gets p = ds = 0 (its warps skip
-// the exponentials).  Roles (12 warps): warp 0 loads the tiles with TMA, warp 1
-// issues the MMAs, warps 4-11 are two softmax warpgroups that take alternate
+// the exponentials).  Roles (12 warps): warp 0 loads the tiles with TMA, warps 1
+// and 2 issue the MMAs, warps 4-11 are two softmax warpgroups that take alternate
 // steps, one thread per TMEM lane.  A step's S and dP live in one of two 128-column
-// TMEM stages; P and dS (bf16) are written over S.  The MMAs of step t+2 follow
-// those that read P and dS of step t in the in-order tensor pipe, so a stage
-// needs no other guard.  Every wait is bounded; on expiry the kernel raises
+// TMEM stages; P (bf16) is written over S and dS over dP.  S and dP are handed over
+// apart: S(t+2) is issued as soon as S(t) is read (dq) or dV has P(t) queued (dkv),
+// so a group starts its next exponentials while dS(t)'s products and dP(t+2) run.
+// An MMA that overwrites P or dS is issued by the warp that issued the one that
+// reads it, and the pipe keeps their order.  Two issuing warps, because the waits
+// between two batches cost the issuer 150 to 400 clocks, which the pipe's short
+// queue does not cover: while one warp waits the other's MMAs run.  Every wait is bounded; on expiry the kernel raises
 // SOL_ERR_TIMEOUT, drains what it issued and frees TMEM.
 constexpr int kThreads = 384;            // 4 control warps + 2 softmax warpgroups
 constexpr int kMaxWords = kMaxKeyBlocks / 32;
@@ -187,7 +191,8 @@ struct Cfg {
 struct Bars {
   uint64_t own_full;                // owned tiles have landed (dkv: TMA) / are in TMEM (dq: softmax threads)
   uint64_t full[5], empty[5];       // ring of streamed tile pairs
-  uint64_t s_full[2], p_full[2];    // S and dP of a step are in TMEM; P and dS are
+  uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
+  uint64_t p_full[2], ds_full[2];   // S is read (dq) or P is in its place (dkv) / dS is in dP's place
   uint64_t final_mma;
 };
 
@@ -224,6 +229,16 @@ __device__ __forceinline__ void load_pair4(uint8_t* dst, const CUtensorMap* m1, 
   }
 }
 
+// Position in the ring of streamed tiles: stage and the parity of its current load.
+template <int S>
+struct RingPos {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == S) { s = 0; ph ^= 1u; }
+  }
+};
+
 // Streamed-tile descriptors: as B operand with the head dims as K (K-major), and
 // with the rows as K (MN-major).
 template <int D>
@@ -250,8 +265,11 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
   if (tid == 0) {
     mbar_init(&bar.own_full, 256);
     for (int s = 0; s < C::kDqStages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
-    for (int s = 0; s < 2; ++s) { mbar_init(&bar.s_full[s], 1); mbar_init(&bar.p_full[s], 4); }
-    mbar_init(&bar.final_mma, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.s_full[s], 1); mbar_init(&bar.dp_full[s], 1);
+      mbar_init(&bar.p_full[s], 4); mbar_init(&bar.ds_full[s], 4);
+    }
+    mbar_init(&bar.final_mma, 2);
     x.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -321,45 +339,50 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         if (cnt) drain_bar(&bar.full[s], (cnt - 1) & 1, a.status);
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 2) {
     constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
+    constexpr uint64_t kStep = 2 * (C::kSTile >> 4);   // descriptor step per ring stage
     const uint64_t sd0 = sdesc(smem_u32(ring), 16, 1024), gd0 = sdesc(smem_u32(ring), C::kSChunk, 1024);
-    auto stage_off = [&](int t) { return (uint64_t)((t % C::kDqStages) * 2 * (C::kSTile >> 4)); };
-    auto products = [&](int t) {   // S(t), dP(t)
-      const uint32_t st = tmem + C::kStage + 128 * (t & 1);
-      const uint64_t kd = sd0 + stage_off(t), vd = kd + (C::kSTile >> 4);
+    RingPos<C::kDqStages> ld, use;   // the next step to start, the step to finish
+    auto wait_ld = [&]() { return wait_bar(&bar.full[ld.s], ld.ph, abort_flag, a.status); };
+    // A(TMEM) times a streamed tile: S from Q and K, dP from dO and V
+    auto start = [&](uint32_t col, uint32_t own, uint64_t bd, uint64_t* done) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ts_w(st, tmem + C::kQ + kk * 8, kmaj<D>(kd, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ts_w(st + 64, tmem + C::kDo + kk * 8, kmaj<D>(vd, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
-      mma_commit_w(&bar.s_full[t & 1]);
-    };
-    auto wait_kv = [&](int t) {
-      return __all_sync(0xffffffffu, wait_bar(&bar.full[t % C::kDqStages], (t / C::kDqStages) & 1, abort_flag, a.status));
+        mma_ts_w(tmem + col, tmem + own + kk * 8, kmaj<D>(bd + ld.s * kStep, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+      mma_commit_w(done);
+      ld.next();
     };
     bool ok = T == 0 || __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
     fence_after();
-    for (int t = 0; t < 2 && t < T && ok; ++t)
-      if ((ok = wait_kv(t))) products(t);
-    for (int t = 0; t < T && ok; ++t) {
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.p_full[t & 1], (t >> 1) & 1, abort_flag, a.status));
-      if (!ok) break;
-      fence_after();
-      const uint32_t ds = tmem + C::kStage + 128 * (t & 1);
-      const uint64_t kd = gd0 + stage_off(t);
+    if (warp == 1) {   // S(t+2) once S(t) is in the softmax threads' registers
+      for (int t = 0; t < T && ok; ++t) {
+        ok = wait_ld();
+        if (t >= 2) ok = ok && wait_bar(&bar.p_full[t & 1], ((t >> 1) & 1) ^ 1, abort_flag, a.status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        fence_after();
+        start(C::kStage + 128 * (t & 1), C::kQ, sd0, &bar.s_full[t & 1]);
+      }
+    } else {           // dQ += dS(t) K, then dP(t+2) over dS(t)
+      for (int t = 0; t < 2 && t < T && ok; ++t)
+        if ((ok = __all_sync(0xffffffffu, wait_ld()))) start(C::kStage + 128 * t + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t]);
+      for (int t = 0; t < T && ok; ++t) {
+        const bool more = t + 2 < T;
+        ok = !more || wait_ld();
+        ok = ok && wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        fence_after();
+        const uint32_t ds = C::kStage + 128 * (t & 1) + 64;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_ts_w(tmem + C::kDq, ds + kk * 8, kd + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
-      mma_commit_w(&bar.empty[t % C::kDqStages]);
-      if (t + 2 < T) {
-        if (!(ok = wait_kv(t + 2))) break;
-        products(t + 2);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_w(tmem + C::kDq, tmem + ds + kk * 8, gd0 + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
+        mma_commit_w(&bar.empty[use.s]);   // S(t), on which dS(t) depends, has read its tile too
+        use.next();
+        if (more) start(ds, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t & 1]);
       }
     }
     mma_commit_w(&bar.final_mma);
-    drain_bar(&bar.final_mma, 0, a.status);
+    if (warp == 1) drain_bar(&bar.final_mma, 0, a.status);
   } else if (warp >= 4) {
     const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
     const int row = 64 * i0 + r;
@@ -404,25 +427,48 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
       if (!ok) break;
       fence_after();
       const uint32_t st = lane_addr + C::kStage + 128 * g;
+      float p[64];
+      if (need) {
+        tmem_ld32(st, p);
+        tmem_ld32(st + 32, p + 32);
+        tmem_wait_ld();
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[g]);
+      if (need) {
+        uint64_t mul2 = sl22;
+        if (add) {   // centroids and the last key block: offsets first (log2 units)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float2 o = reinterpret_cast<const float2*>(add)[c];
+            f2unpack(ffma2(f2pack(p[2 * c], p[2 * c + 1]), sl22, f2pack(o.x, o.y)), p[2 * c], p[2 * c + 1]);
+          }
+          mul2 = f2pack(1.f, 1.f);
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float e0, e1;
+          f2unpack(ffma2(f2pack(p[2 * c], p[2 * c + 1]), mul2, nl2), e0, e1);
+          p[2 * c] = ex2(e0);
+          p[2 * c + 1] = ex2(e1);
+        }
+      }
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.dp_full[g], (t >> 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      fence_after();
       uint32_t pk[32];
       if (need) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          float s[32], dp[32];
-          tmem_ld32(st + 32 * hh, s);
+          float dp[32];
           tmem_ld32(st + 64 + 32 * hh, dp);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            uint64_t e2 = ffma2(f2pack(s[2 * c], s[2 * c + 1]), sl22, nl2);
-            if (add) {
-              const float2 o = reinterpret_cast<const float2*>(add)[16 * hh + c];
-              e2 = fadd2(e2, f2pack(o.x, o.y));
-            }
-            float e0, e1, d0, d1;
-            f2unpack(e2, e0, e1);
-            const uint64_t p2 = f2pack(ex2(e0), ex2(e1));
-            f2unpack(fmul2(p2, fadd2(f2pack(dp[2 * c], dp[2 * c + 1]), nd2)), d0, d1);
+            const int k = 32 * hh + 2 * c;
+            float d0, d1;
+            f2unpack(fmul2(f2pack(p[k], p[k + 1]), fadd2(f2pack(dp[2 * c], dp[2 * c + 1]), nd2)), d0, d1);
             pk[16 * hh + c] = pack_bf16(d0, d1);
           }
         }
@@ -430,11 +476,11 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
 #pragma unroll
         for (int c = 0; c < 32; ++c) pk[c] = 0u;
       }
-      tmem_st32(st, pk);
+      tmem_st32(st + 64, pk);
       tmem_wait_st();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[g]);
+      if (lane == 0) mbar_arrive(&bar.ds_full[g]);
     }
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
     if (ok && !*abort_flag) {
@@ -491,9 +537,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
 
   if (tid == 0) {
     mbar_init(&bar.own_full, 1);
-    for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
-    for (int s = 0; s < 2; ++s) { mbar_init(&bar.s_full[s], 1); mbar_init(&bar.p_full[s], 4); }
-    mbar_init(&bar.final_mma, 1);
+    for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.s_full[s], 1); mbar_init(&bar.dp_full[s], 1);
+      mbar_init(&bar.p_full[s], 4); mbar_init(&bar.ds_full[s], 4);
+    }
+    mbar_init(&bar.final_mma, 2);
     x.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     mbar_expect_tx(&bar.own_full, 2 * C::kOTile);
@@ -573,48 +622,45 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       }
       drain_bar(&bar.own_full, 0, a.status);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 2) {
+    // warp 1: dV += P(t) dO, then S(t+2) over P(t); warp 2: dK += dS(t) Q, then dP(t+2) over dS(t)
     constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
-    const uint64_t kd = sdesc(smem_u32(own), 16, 1024), vd = kd + (C::kOTile >> 4);
-    const uint64_t sd0 = sdesc(smem_u32(ring), 16, 1024), gd0 = sdesc(smem_u32(ring), C::kSChunk, 1024);
-    auto stage_off = [&](int t) { return (uint64_t)((t % S) * 2 * (C::kSTile >> 4)); };
-    auto products = [&](int t) {
-      const uint32_t st = tmem + C::kStage + 128 * (t & 1);
-      const uint64_t qd = sd0 + stage_off(t), od = qd + (C::kSTile >> 4);
+    constexpr uint64_t kStep = 2 * (C::kSTile >> 4);   // descriptor step per ring stage
+    const bool first = warp == 1;
+    const uint64_t tile = C::kSTile >> 4;
+    const uint64_t od = sdesc(smem_u32(own), 16, 1024) + (first ? 0 : C::kOTile >> 4);            // K / V
+    const uint64_t sd = sdesc(smem_u32(ring), 16, 1024) + (first ? 0 : tile);                       // Q / dO, K-major
+    const uint64_t gd = sdesc(smem_u32(ring), C::kSChunk, 1024) + (first ? tile : 0);               // dO / Q, MN-major
+    const uint32_t col = tmem + C::kStage + (first ? 0 : 64), acc = tmem + (first ? C::kDv : C::kDk);
+    uint64_t* done = first ? bar.s_full : bar.dp_full;
+    uint64_t* ready = first ? bar.p_full : bar.ds_full;
+    RingPos<S> ld, use;
+    auto wait_ld = [&]() { return wait_bar(&bar.full[ld.s], ld.ph, abort_flag, a.status); };
+    auto start = [&](int g) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss_w(st, kmaj<D>(kd, kk, C::kOChunk), kmaj<D>(qd, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss_w(st + 64, kmaj<D>(vd, kk, C::kOChunk), kmaj<D>(od, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
-      mma_commit_w(&bar.s_full[t & 1]);
-    };
-    auto wait_ring = [&](int t) {
-      return __all_sync(0xffffffffu, wait_bar(&bar.full[t % S], (t / S) & 1, abort_flag, a.status));
+        mma_ss_w(col + 128 * g, kmaj<D>(od, kk, C::kOChunk), kmaj<D>(sd + ld.s * kStep, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+      mma_commit_w(&done[g]);
+      ld.next();
     };
     bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
     for (int t = 0; t < 2 && t < T && ok; ++t)
-      if ((ok = wait_ring(t))) products(t);
+      if ((ok = __all_sync(0xffffffffu, wait_ld()))) start(t);
     for (int t = 0; t < T && ok; ++t) {
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.p_full[t & 1], (t >> 1) & 1, abort_flag, a.status));
-      if (!ok) break;
+      const bool more = t + 2 < T;
+      ok = !more || wait_ld();
+      ok = ok && wait_bar(&ready[t & 1], (t >> 1) & 1, abort_flag, a.status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       fence_after();
-      const uint32_t st = tmem + C::kStage + 128 * (t & 1);
-      const uint64_t qd = gd0 + stage_off(t), od = qd + (C::kSTile >> 4);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_ts_w(tmem + C::kDv, st + kk * 8, od + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_ts_w(tmem + C::kDk, st + 32 + kk * 8, qd + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
-      mma_commit_w(&bar.empty[t % S]);
-      if (t + 2 < T) {
-        if (!(ok = wait_ring(t + 2))) break;
-        products(t + 2);
-      }
+        mma_ts_w(acc, col + 128 * (t & 1) + kk * 8, gd + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
+      mma_commit_w(&bar.empty[use.s]);
+      use.next();
+      if (more) start(t & 1);
     }
     mma_commit_w(&bar.final_mma);
-    drain_bar(&bar.final_mma, 0, a.status);
+    if (first) drain_bar(&bar.final_mma, 0, a.status);
   } else if (warp >= 4) {
     const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
@@ -649,44 +695,65 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (!ok) break;
       fence_after();
       const uint32_t st = lane_addr + C::kStage + 128 * g;
-      uint32_t pp[32], pd[32];
+      float p[64];
+      uint32_t pk[32];
       if (need) {
+        tmem_ld32(st, p);
+        tmem_ld32(st + 32, p + 32);
+        tmem_wait_ld();
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float s[32], dp[32];
-          tmem_ld32(st + 32 * hh, s);
-          tmem_ld32(st + 64 + 32 * hh, dp);
-          tmem_wait_ld();
+        for (int c = 0; c < 16; ++c) {
+          const float4 l4 = reinterpret_cast<const float4*>(x.nl[rs])[c];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 l4 = reinterpret_cast<const float4*>(x.nl[rs])[8 * hh + c];
-            const float4 d4 = reinterpret_cast<const float4*>(x.nd[rs])[8 * hh + c];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint64_t l2 = u ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y);
-              const uint64_t n2 = u ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y);
-              if (kCent) l2 = fadd2(l2, add2);
-              const int k = 4 * c + 2 * u;
-              float e0, e1, d0, d1;
-              f2unpack(ffma2(f2pack(s[k], s[k + 1]), sl22, l2), e0, e1);
-              const float p0 = ex2(e0), p1 = ex2(e1);
-              f2unpack(fmul2(f2pack(p0, p1), fadd2(f2pack(dp[k], dp[k + 1]), n2)), d0, d1);
-              if (kCent) gbs += d0 + d1;
-              pp[16 * hh + 2 * c + u] = pack_bf16(p0, p1);
-              pd[16 * hh + 2 * c + u] = pack_bf16(d0, d1);
-            }
+          for (int u = 0; u < 2; ++u) {
+            uint64_t l2 = u ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y);
+            if (kCent) l2 = fadd2(l2, add2);
+            const int k = 4 * c + 2 * u;
+            float e0, e1;
+            f2unpack(ffma2(f2pack(p[k], p[k + 1]), sl22, l2), e0, e1);
+            p[k] = ex2(e0);
+            p[k + 1] = ex2(e1);
+            pk[2 * c + u] = pack_bf16(p[k], p[k + 1]);
           }
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pp[c] = pd[c] = 0u;
+        for (int c = 0; c < 32; ++c) pk[c] = 0u;
       }
-      tmem_st32(st, pp);
-      tmem_st32(st + 32, pd);
+      tmem_st32(st, pk);
       tmem_wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full[g]);
+      ok = __all_sync(0xffffffffu, wait_bar(&bar.dp_full[g], (t >> 1) & 1, abort_flag, a.status));
+      if (!ok) break;
+      fence_after();
+      if (need) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float dp[32];
+          tmem_ld32(st + 64 + 32 * hh, dp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 d4 = reinterpret_cast<const float4*>(x.nd[rs])[8 * hh + c];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint64_t n2 = u ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y);
+              const int k = 4 * c + 2 * u;
+              float d0, d1;
+              f2unpack(fmul2(f2pack(p[32 * hh + k], p[32 * hh + k + 1]), fadd2(f2pack(dp[k], dp[k + 1]), n2)), d0, d1);
+              if (kCent) gbs += d0 + d1;
+              pk[16 * hh + 2 * c + u] = pack_bf16(d0, d1);
+            }
+          }
+        }
+      }
+      tmem_st32(st + 64, pk);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.ds_full[g]);
     }
     if (kCent && g == 0) x.gb[r] = gbs;
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
