@@ -193,17 +193,17 @@ struct Bars {
   uint64_t full[5], empty[5];       // ring of streamed tile pairs
   uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
   uint64_t p_full[2], ds_full[2];   // S is read (dq) or P is in its place (dkv) / dS is in dP's place
+  uint64_t cent_ready;              // dq: the centroids' offsets are in shared memory
   uint64_t final_mma;
 };
 
 struct DqExtra {
   Bars bar;
   uint32_t tmem_base;
-  int abort_flag, n_union, n_cent;
+  int abort_flag, n_union;
   uint32_t sel[2][kMaxWords];
   int list[kMaxKeyBlocks];                        // union entries: j | needA << 16 | needB << 17
-  int cent[16];                                   // 64-centroid units: u | liveA << 16 | liveB << 17
-  alignas(16) float cent_add[16][2][64];          // log2-unit offsets, -inf where masked
+  alignas(16) float cent_add[16][2][64];          // 64-centroid units' offsets (log2 units), -inf where masked
   alignas(16) float tail_add[64];                 // 0 for valid rows of the last key block, -inf past N
 };
 
@@ -264,6 +264,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
 
   if (tid == 0) {
     mbar_init(&bar.own_full, 256);
+    mbar_init(&bar.cent_ready, 1);
     for (int s = 0; s < C::kDqStages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.s_full[s], 1); mbar_init(&bar.dp_full[s], 1);
@@ -279,6 +280,19 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
   }
   const int n_tail = a.N - 64 * (a.nb - 1);
   if (tid < 64) x.tail_add[tid] = tid < n_tail ? 0.f : -INFINITY;
+  // The softmax threads' rows of Q (group 0) and dO (group 1), loaded now so that
+  // they arrive beside the plan (rows past N as zeros).
+  const int row = 64 * i0 + (tid & 127);
+  uint4 rows[D / 8];
+  if (warp >= 4) {
+    const __nv_bfloat16* src = warp < 8 ? a.q + (int64_t)b * a.sb + (int64_t)row * a.sn + (int64_t)h * a.sh
+                                        : a.d_o + (int64_t)b * a.ob + (int64_t)row * a.on + (int64_t)h * a.oh;
+#pragma unroll
+    for (int u = 0; u < D / 8; ++u) {
+      rows[u] = make_uint4(0, 0, 0, 0);
+      if (row < a.N) rows[u] = reinterpret_cast<const uint4*>(src)[u];
+    }
+  }
   {
     const int* P = a.plan + (bh * ntq + tq) * plan_ints(mw, a.nb);
     for (int e = tid; e < 2 * mw + a.nb; e += kThreads) {
@@ -288,8 +302,13 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     }
     if (tid == 0) x.n_union = P[0];
   }
+  fence_before();
   cta_sync();
-  if (warp == 0) {   // 64-centroid units that either query block leaves to its centroids
+  fence_after();
+  const uint32_t tmem = x.tmem_base;
+  // 64-centroid units that either query block leaves to its centroids (every warp for itself)
+  uint32_t live0, live1;
+  {
     const int units = a.centroids ? (a.nb + 63) / 64 : 0;
     bool l0 = false, l1 = false;
     if (lane < units) {
@@ -299,21 +318,15 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         l1 |= i0 + 1 < a.nb && (~x.sel[1][w] & vm) != 0u;
       }
     }
-    const uint32_t any = __ballot_sync(0xffffffffu, l0 || l1);
-    if (l0 || l1) x.cent[__popc(any & ((1u << lane) - 1u))] = lane | (int)l0 << 16 | (int)l1 << 17;
-    if (lane == 0) x.n_cent = __popc(any);
+    live0 = __ballot_sync(0xffffffffu, l0);
+    live1 = __ballot_sync(0xffffffffu, l1);
   }
-  cta_sync();
-  for (int e = tid; e < 128 * x.n_cent; e += kThreads) {
-    const int slot = e >> 7, hf = (e >> 6) & 1, c = e & 63, j = 64 * (x.cent[slot] & 0xffff) + c;
-    const bool live = j < a.nb && i0 + hf < a.nb && !((x.sel[hf][j >> 5] >> (j & 31)) & 1u);
-    x.cent_add[slot][hf][c] = live ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
-  }
-  fence_before();
-  cta_sync();
-  fence_after();
-  const uint32_t tmem = x.tmem_base;
-  const int T = x.n_union + x.n_cent;
+  const int n_union = x.n_union, T = n_union + __popc(live0 | live1);
+  auto unit = [&](int t) {   // of step t >= n_union
+    uint32_t m = live0 | live1;
+    for (int k = t - n_union; k > 0; --k) m &= m - 1;
+    return __ffs(m) - 1;
+  };
 
   if (warp == 0) {
     if (lane == 0) {   // K and V (centroid) tiles
@@ -324,10 +337,10 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         uint8_t* dst = ring + s * 2 * C::kSTile;
         ++nl;
         mbar_expect_tx(&bar.full[s], 2 * C::kSTile);
-        if (t < x.n_union) {
+        if (t < n_union) {
           load_pair4<D>(dst, &mk, &mv, 64 * (x.list[t] & 0xffff), h, b, &bar.full[s]);
         } else {
-          const int row = 64 * (x.cent[t - x.n_union] & 0xffff);
+          const int row = 64 * unit(t);
           for (int c = 0; c < C::kChunks; ++c) {
             tma_load_3d(dst + c * C::kSChunk, &mkb, c * 64, row, (int)bh, &bar.full[s]);
             tma_load_3d(dst + C::kSTile + c * C::kSChunk, &mvb, c * 64, row, (int)bh, &bar.full[s]);
@@ -345,32 +358,51 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     const uint64_t sd0 = sdesc(smem_u32(ring), 16, 1024), gd0 = sdesc(smem_u32(ring), C::kSChunk, 1024);
     RingPos<C::kDqStages> ld, use;   // the next step to start, the step to finish
     auto wait_ld = [&]() { return wait_bar(&bar.full[ld.s], ld.ph, abort_flag, a.status); };
-    // A(TMEM) times a streamed tile: S from Q and K, dP from dO and V
-    auto start = [&](uint32_t col, uint32_t own, uint64_t bd, uint64_t* done) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ts_w(tmem + col, tmem + own + kk * 8, kmaj<D>(bd + ld.s * kStep, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
-      mma_commit_w(done);
+    // A(TMEM) times a streamed tile: S from Q and K, dP from dO and V.  Half-way
+    // through, the next step's barriers are looked at: the answer comes back while
+    // the second half is issued, and a step whose barriers are already complete
+    // (the usual case) starts without a wait.
+    auto start = [&](uint32_t col, uint32_t own, uint64_t bd, uint64_t* done, auto&& probe) {
+      const uint64_t b0 = bd + ld.s * kStep;
       ld.next();
+      bool r = false;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        if (kk == D / 32) r = probe();
+        mma_ts_w(tmem + col, tmem + own + kk * 8, kmaj<D>(b0, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_w(done);
+      return r;
     };
     bool ok = T == 0 || __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
     fence_after();
     if (warp == 1) {   // S(t+2) once S(t) is in the softmax threads' registers
+      bool early = false;
       for (int t = 0; t < T && ok; ++t) {
-        ok = wait_ld();
-        if (t >= 2) ok = ok && wait_bar(&bar.p_full[t & 1], ((t >> 1) & 1) ^ 1, abort_flag, a.status);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const uint32_t par = ((t >> 1) & 1) ^ 1;
+        if (!__all_sync(0xffffffffu, early)) {
+          ok = wait_ld() && (t < 2 || wait_bar(&bar.p_full[t & 1], par, abort_flag, a.status));
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
         fence_after();
-        start(C::kStage + 128 * (t & 1), C::kQ, sd0, &bar.s_full[t & 1]);
+        early = start(C::kStage + 128 * (t & 1), C::kQ, sd0, &bar.s_full[t & 1], [&]() {
+          const int u = t + 1;
+          const bool l = mbar_test(&bar.full[ld.s], ld.ph);
+          return (u < 2 || mbar_test(&bar.p_full[u & 1], ((u >> 1) & 1) ^ 1)) && l;
+        });
       }
     } else {           // dQ += dS(t) K, then dP(t+2) over dS(t)
       for (int t = 0; t < 2 && t < T && ok; ++t)
-        if ((ok = __all_sync(0xffffffffu, wait_ld()))) start(C::kStage + 128 * t + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t]);
+        if ((ok = __all_sync(0xffffffffu, wait_ld())))
+          start(C::kStage + 128 * t + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t], []() { return false; });
+      bool early = false;
       for (int t = 0; t < T && ok; ++t) {
         const bool more = t + 2 < T;
-        ok = !more || wait_ld();
-        ok = ok && wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (!__all_sync(0xffffffffu, early)) {
+          ok = !more || wait_ld();
+          ok = ok && wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
         fence_after();
         const uint32_t ds = C::kStage + 128 * (t & 1) + 64;
 #pragma unroll
@@ -378,26 +410,38 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
           mma_ts_w(tmem + C::kDq, tmem + ds + kk * 8, gd0 + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
         mma_commit_w(&bar.empty[use.s]);   // S(t), on which dS(t) depends, has read its tile too
         use.next();
-        if (more) start(ds, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t & 1]);
+        early = false;
+        if (more)
+          early = start(ds, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t & 1], [&]() {
+            const bool l = t + 3 >= T || mbar_test(&bar.full[ld.s], ld.ph);
+            return mbar_test(&bar.ds_full[(t + 1) & 1], ((t + 1) >> 1) & 1) && l;
+          });
       }
     }
     mma_commit_w(&bar.final_mma);
     if (warp == 1) drain_bar(&bar.final_mma, 0, a.status);
+  } else if (warp == 3) {   // the centroids' offsets, needed after the last listed block
+    for (int u = 0; u < 16; ++u) {
+      if (!(((live0 | live1) >> u) & 1u)) continue;
+      for (int e = lane; e < 128; e += 32) {
+        const int hf = e >> 6, j = 64 * u + (e & 63);
+        const bool live = j < a.nb && i0 + hf < a.nb && !((x.sel[hf][j >> 5] >> (j & 31)) & 1u);
+        x.cent_add[u][hf][e & 63] = live ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.cent_ready);
   } else if (warp >= 4) {
     const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
-    const int row = 64 * i0 + r;
     const bool valid = row < a.N;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
-    {   // group 0 puts Q, group 1 dO into TMEM (rows past N as zeros)
-      const __nv_bfloat16* src = g == 0 ? a.q + (int64_t)b * a.sb + (int64_t)row * a.sn + (int64_t)h * a.sh
-                                        : a.d_o + (int64_t)b * a.ob + (int64_t)row * a.on + (int64_t)h * a.oh;
+    {   // group 0 puts Q, group 1 dO into TMEM
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint32_t w[32];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (valid) v = reinterpret_cast<const uint4*>(src + 64 * c)[u];
+          const uint4 v = rows[8 * c + u];
           w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
         }
         tmem_st32(lane_addr + (g == 0 ? C::kQ : C::kDo) + 32 * c, w);
@@ -415,13 +459,16 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     for (int t = g; t < T && ok; t += 2) {
       bool need;
       const float* add = nullptr;
-      if (t < x.n_union) {
+      if (t < n_union) {
         const int e = x.list[t];
         need = (e >> (16 + hf)) & 1;
         if ((e & 0xffff) == a.nb - 1) add = x.tail_add;
       } else {
-        need = (x.cent[t - x.n_union] >> (16 + hf)) & 1;
-        add = x.cent_add[t - x.n_union][hf];
+        if (t < n_union + 2) ok = __all_sync(0xffffffffu, wait_bar(&bar.cent_ready, 0, abort_flag, a.status));
+        if (!ok) break;
+        const int u = unit(t);
+        need = ((hf ? live1 : live0) >> u) & 1u;
+        add = x.cent_add[u][hf];
       }
       ok = __all_sync(0xffffffffu, wait_bar(&bar.s_full[g], (t >> 1) & 1, abort_flag, a.status));
       if (!ok) break;
@@ -678,7 +725,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         x.gsum[which][half][d] = v;
       }
     }
-    float gbs = 0.f;
+    uint64_t gb2 = 0ull;   // kCent: the sums of ds of even and odd queries
     bool ok = true;
     for (int t = g; t < T && ok; t += 2) {
       const int rs = t % S;
@@ -742,8 +789,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
               const uint64_t n2 = u ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y);
               const int k = 4 * c + 2 * u;
               float d0, d1;
-              f2unpack(fmul2(f2pack(p[32 * hh + k], p[32 * hh + k + 1]), fadd2(f2pack(dp[k], dp[k + 1]), n2)), d0, d1);
-              if (kCent) gbs += d0 + d1;
+              const uint64_t d2 = fmul2(f2pack(p[32 * hh + k], p[32 * hh + k + 1]), fadd2(f2pack(dp[k], dp[k + 1]), n2));
+              if (kCent) gb2 = fadd2(gb2, d2);
+              f2unpack(d2, d0, d1);
               pk[16 * hh + 2 * c + u] = pack_bf16(d0, d1);
             }
           }
@@ -755,6 +803,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ds_full[g]);
     }
+    float gbs, gb_odd;
+    f2unpack(gb2, gbs, gb_odd);
+    gbs += gb_odd;
     if (kCent && g == 0) x.gb[r] = gbs;
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
     __syncwarp();
@@ -829,19 +880,11 @@ template <int D>
 __global__ void __launch_bounds__(256) pool_bwd_kernel(const BwdArgs a) {
   constexpr int LPR = D / 8, G = 256 / LPR, R = 64 / G;   // rows a lane group holds
   __shared__ float sw[64], sh[64], red[G][D], cst[4];
+  __shared__ alignas(16) float sg[2][D];
   const int j = blockIdx.y;
   const int64_t bh = blockIdx.x, bhs = (int64_t)a.B * a.H;
   const int b = (int)(bh / a.H), h = (int)(bh % a.H);
   const int c = threadIdx.x % LPR, g = threadIdx.x / LPR, n = min(64, a.N - 64 * j);
-  float an[8], gk[8], gv[8], gb = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) { an[i] = a.anchor[bh * D + 8 * c + i]; gk[i] = gv[i] = 0.f; }
-  for (int s = 0; s < a.splits; ++s) {
-    const int64_t at = (s * bhs + bh) * a.nb + j;
-    gb += a.gb_[at];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { gk[i] += a.gk[at * D + 8 * c + i]; gv[i] += a.gv[at * D + 8 * c + i]; }
-  }
   uint4 kr[R], vr[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -851,6 +894,22 @@ __global__ void __launch_bounds__(256) pool_bwd_kernel(const BwdArgs a) {
     if (r < n) kr[i] = *reinterpret_cast<const uint4*>(a.k + at);
     if (r < n && a.mode == 2) vr[i] = *reinterpret_cast<const uint4*>(a.v + at);
   }
+  // the block's gk and gv, summed over the query ranges in order (one dim of one of them a thread)
+  for (int e = threadIdx.x; e < 2 * D; e += 256) {
+    const float* src = (e < D ? a.gk : a.gv) + (bh * a.nb + j) * D + e % D;
+    float v = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) v += src[s * bhs * a.nb * D];
+    sg[e / D][e % D] = v;
+  }
+  float an[8], gk[8], gv[8], gb = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < a.splits; ++s) gb += a.gb_[(s * bhs + bh) * a.nb + j];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) an[i] = a.anchor[bh * D + 8 * c + i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) { gk[i] = sg[0][8 * c + i]; gv[i] = sg[1][8 * c + i]; }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float f[8], w[8], e = 0.f, hh = 0.f;
