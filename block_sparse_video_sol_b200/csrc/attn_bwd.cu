@@ -143,8 +143,13 @@ __global__ void __launch_bounds__(kTWarps * 32) tplan_kernel(const BwdArgs a) {
 //                transposed: S = K Q^T, dP = V dO^T, dV += P dO, dK += dS Q.  P and
 //                dS come out with their rows in TMEM lanes, as an A operand needs.
 //
-// A half of the tile that a step does not concern gets p = ds = 0 (its warps skip
-// the exponentials).  Roles (12 warps): warp 0 loads the tiles with TMA, warps 1
+// A half of the tile (64 of its 128 rows) that a step does not concern is left out
+// of that step's MMAs by their row mask, and its softmax warps only pass the
+// barriers on: the MMA takes the same time, but a masked row costs no power.  On
+// lists whose steps mostly concern one half this is what sets the clock of long
+// calls (a loop of such MMAs, 148 SMs at the 1 kW limit: 1.58 GHz unmasked, 1.85
+// GHz with half the rows masked).  Accumulators start from zeros stored by the
+// softmax threads, since a half's first step may not be the tile's.  Roles (12 warps): warp 0 loads the tiles with TMA, warps 1
 // and 2 issue the MMAs, warps 4-11 are two softmax warpgroups that take alternate
 // steps, one thread per TMEM lane.  A step's S and dP live in one of two 128-column
 // TMEM stages; P (bf16) is written over S and dS over dP.  S and dP are handed over
@@ -200,10 +205,11 @@ struct Bars {
 struct DqExtra {
   Bars bar;
   uint32_t tmem_base;
-  int abort_flag, n_union;
+  int abort_flag, n_union, n_cent;
   uint32_t sel[2][kMaxWords];
   int list[kMaxKeyBlocks];                        // union entries: j | needA << 16 | needB << 17
-  alignas(16) float cent_add[16][2][64];          // 64-centroid units' offsets (log2 units), -inf where masked
+  int clist[16];                                  // 64-centroid units: u | liveA << 16 | liveB << 17
+  alignas(16) float cent_add[16][2][64];          // their offsets (log2 units), -inf where masked
   alignas(16) float tail_add[64];                 // 0 for valid rows of the last key block, -inf past N
 };
 
@@ -228,6 +234,9 @@ __device__ __forceinline__ void load_pair4(uint8_t* dst, const CUtensorMap* m1, 
     tma_load_4d(dst + Cfg<D>::kSTile + c * Cfg<D>::kSChunk, m2, c * 64, h, row, b, bar);
   }
 }
+
+// Rows of half hf that a step with this list entry leaves out of its MMAs.
+__device__ __forceinline__ uint32_t off(int entry, int hf) { return (entry >> (16 + hf)) & 1 ? 0u : 0xffffffffu; }
 
 // Position in the ring of streamed tiles: stage and the parity of its current load.
 template <int S>
@@ -300,34 +309,20 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
       if (e >= 2 * mw) x.list[e - 2 * mw] = v;
       else x.sel[e / mw][e % mw] = (uint32_t)v;
     }
-    if (tid == 0) x.n_union = P[0];
+    if (tid < 32) {   // 64-centroid units (two bitmap words) that either query block leaves to its centroids
+      const uint32_t w0 = (uint32_t)P[12], w1 = (uint32_t)P[13];
+      const bool l0 = tid < 16 && ((w0 >> (2 * tid)) & 3u), l1 = tid < 16 && ((w1 >> (2 * tid)) & 3u);
+      const uint32_t any = __ballot_sync(0xffffffffu, l0 || l1);
+      if (l0 || l1) x.clist[__popc(any & ((1u << tid) - 1u))] = tid | (int)l0 << 16 | (int)l1 << 17;
+      if (tid == 0) { x.n_union = P[0]; x.n_cent = __popc(any); }
+    }
   }
   fence_before();
   cta_sync();
   fence_after();
   const uint32_t tmem = x.tmem_base;
-  // 64-centroid units that either query block leaves to its centroids (every warp for itself)
-  uint32_t live0, live1;
-  {
-    const int units = a.centroids ? (a.nb + 63) / 64 : 0;
-    bool l0 = false, l1 = false;
-    if (lane < units) {
-      for (int w = 2 * lane; w < 2 * lane + 2 && w < mw; ++w) {
-        const uint32_t vm = a.nb - 32 * w >= 32 ? 0xffffffffu : (1u << (a.nb - 32 * w)) - 1u;
-        l0 |= (~x.sel[0][w] & vm) != 0u;
-        l1 |= i0 + 1 < a.nb && (~x.sel[1][w] & vm) != 0u;
-      }
-    }
-    live0 = __ballot_sync(0xffffffffu, l0);
-    live1 = __ballot_sync(0xffffffffu, l1);
-  }
-  const int n_union = x.n_union, T = n_union + __popc(live0 | live1);
-  auto unit = [&](int t) {   // of step t >= n_union
-    uint32_t m = live0 | live1;
-    for (int k = t - n_union; k > 0; --k) m &= m - 1;
-    return __ffs(m) - 1;
-  };
-
+  const int n_union = x.n_union, T = n_union + x.n_cent;
+  auto entry = [&](int t) { return *(t < n_union ? &x.list[t] : &x.clist[t - n_union]); };
   if (warp == 0) {
     if (lane == 0) {   // K and V (centroid) tiles
       int nl = 0;
@@ -340,7 +335,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         if (t < n_union) {
           load_pair4<D>(dst, &mk, &mv, 64 * (x.list[t] & 0xffff), h, b, &bar.full[s]);
         } else {
-          const int row = 64 * unit(t);
+          const int row = 64 * (x.clist[t - n_union] & 0xffff);
           for (int c = 0; c < C::kChunks; ++c) {
             tma_load_3d(dst + c * C::kSChunk, &mkb, c * 64, row, (int)bh, &bar.full[s]);
             tma_load_3d(dst + C::kSTile + c * C::kSChunk, &mvb, c * 64, row, (int)bh, &bar.full[s]);
@@ -362,22 +357,23 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     // through, the next step's barriers are looked at: the answer comes back while
     // the second half is issued, and a step whose barriers are already complete
     // (the usual case) starts without a wait.
-    auto start = [&](uint32_t col, uint32_t own, uint64_t bd, uint64_t* done, auto&& probe) {
+    auto start = [&](uint32_t col, uint32_t own, uint64_t bd, uint64_t* done, int e, auto&& probe) {
       const uint64_t b0 = bd + ld.s * kStep;
       ld.next();
       bool r = false;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         if (kk == D / 32) r = probe();
-        mma_ts_w(tmem + col, tmem + own + kk * 8, kmaj<D>(b0, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+        mma_ts_m(tmem + col, tmem + own + kk * 8, kmaj<D>(b0, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u, off(e, 0), off(e, 1));
       }
       mma_commit_w(done);
       return r;
     };
-    bool ok = T == 0 || __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
+    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
     fence_after();
     if (warp == 1) {   // S(t+2) once S(t) is in the softmax threads' registers
       bool early = false;
+      int e0 = T > 0 ? entry(0) : 0;
       for (int t = 0; t < T && ok; ++t) {
         const uint32_t par = ((t >> 1) & 1) ^ 1;
         if (!__all_sync(0xffffffffu, early)) {
@@ -385,49 +381,58 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
         fence_after();
-        early = start(C::kStage + 128 * (t & 1), C::kQ, sd0, &bar.s_full[t & 1], [&]() {
+        const int e = e0;
+        early = start(C::kStage + 128 * (t & 1), C::kQ, sd0, &bar.s_full[t & 1], e, [&]() {
           const int u = t + 1;
           const bool l = mbar_test(&bar.full[ld.s], ld.ph);
+          e0 = entry(min(u, T - 1));
           return (u < 2 || mbar_test(&bar.p_full[u & 1], ((u >> 1) & 1) ^ 1)) && l;
         });
       }
     } else {           // dQ += dS(t) K, then dP(t+2) over dS(t)
       for (int t = 0; t < 2 && t < T && ok; ++t)
         if ((ok = __all_sync(0xffffffffu, wait_ld())))
-          start(C::kStage + 128 * t + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t], []() { return false; });
+          start(C::kStage + 128 * t + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t], entry(t), []() { return false; });
+      auto dq_mma = [&](int t, int e) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_m(tmem + C::kDq, tmem + C::kStage + 128 * (t & 1) + 64 + kk * 8, gd0 + use.s * kStep + (uint64_t)(kk * 2048 >> 4),
+                   id_g, 1u, off(e, 0), off(e, 1));
+        mma_commit_w(&bar.empty[use.s]);   // S(t), on which dS(t) depends, has read its tile too
+        use.next();
+      };
       bool early = false;
-      for (int t = 0; t < T && ok; ++t) {
-        const bool more = t + 2 < T;
+      int t = 0, e0 = T > 0 ? entry(0) : 0, e1 = T > 1 ? entry(1) : 0, e2 = T > 2 ? entry(2) : 0;   // steps t, t+1, t+2
+      for (; t < T - 2 && ok; ++t) {   // (no condition around a batch: see the last two steps below)
         if (!__all_sync(0xffffffffu, early)) {
-          ok = !more || wait_ld();
-          ok = ok && wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status);
+          ok = wait_ld() && wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
         fence_after();
-        const uint32_t ds = C::kStage + 128 * (t & 1) + 64;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ts_w(tmem + C::kDq, tmem + ds + kk * 8, gd0 + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
-        mma_commit_w(&bar.empty[use.s]);   // S(t), on which dS(t) depends, has read its tile too
-        use.next();
-        early = false;
-        if (more)
-          early = start(ds, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t & 1], [&]() {
-            const bool l = t + 3 >= T || mbar_test(&bar.full[ld.s], ld.ph);
-            return mbar_test(&bar.ds_full[(t + 1) & 1], ((t + 1) >> 1) & 1) && l;
-          });
+        dq_mma(t, e0);
+        const int e = e2;
+        e0 = e1;
+        e1 = e2;
+        early = start(C::kStage + 128 * (t & 1) + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t & 1], e, [&]() {
+          const bool l = mbar_test(&bar.full[ld.s], ld.ph);
+          e2 = entry(min(t + 3, T - 1));
+          return mbar_test(&bar.ds_full[(t + 1) & 1], ((t + 1) >> 1) & 1) && l;
+        });
+      }
+      for (; t < T && ok; ++t) {
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status)))) break;
+        fence_after();
+        dq_mma(t, e0);
+        e0 = e1;
       }
     }
     mma_commit_w(&bar.final_mma);
     if (warp == 1) drain_bar(&bar.final_mma, 0, a.status);
   } else if (warp == 3) {   // the centroids' offsets, needed after the last listed block
-    for (int u = 0; u < 16; ++u) {
-      if (!(((live0 | live1) >> u) & 1u)) continue;
-      for (int e = lane; e < 128; e += 32) {
-        const int hf = e >> 6, j = 64 * u + (e & 63);
-        const bool live = j < a.nb && i0 + hf < a.nb && !((x.sel[hf][j >> 5] >> (j & 31)) & 1u);
-        x.cent_add[u][hf][e & 63] = live ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
-      }
+    for (int e = lane; e < 128 * x.n_cent; e += 32) {
+      const int slot = e >> 7, hf = (e >> 6) & 1, j = 64 * (x.clist[slot] & 0xffff) + (e & 63);
+      const bool live = j < a.nb && i0 + hf < a.nb && !((x.sel[hf][j >> 5] >> (j & 31)) & 1u);
+      x.cent_add[slot][hf][e & 63] = live ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar.cent_ready);
@@ -445,6 +450,9 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
           w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
         }
         tmem_st32(lane_addr + (g == 0 ? C::kQ : C::kDo) + 32 * c, w);
+#pragma unroll
+        for (int u = 0; u < 32; ++u) w[u] = 0u;
+        tmem_st32(lane_addr + C::kDq + g * (D / 2) + 32 * c, w);   // dQ starts from zero (its half)
       }
       tmem_wait_st();
       fence_before();
@@ -457,18 +465,15 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     const uint64_t sl22 = f2pack(sl2, sl2), nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
     bool ok = true;
     for (int t = g; t < T && ok; t += 2) {
-      bool need;
       const float* add = nullptr;
+      const int e = entry(t);
+      const bool need = (e >> (16 + hf)) & 1;
       if (t < n_union) {
-        const int e = x.list[t];
-        need = (e >> (16 + hf)) & 1;
         if ((e & 0xffff) == a.nb - 1) add = x.tail_add;
       } else {
         if (t < n_union + 2) ok = __all_sync(0xffffffffu, wait_bar(&bar.cent_ready, 0, abort_flag, a.status));
         if (!ok) break;
-        const int u = unit(t);
-        need = ((hf ? live1 : live0) >> u) & 1u;
-        add = x.cent_add[u][hf];
+        add = x.cent_add[t - n_union][hf];
       }
       ok = __all_sync(0xffffffffu, wait_bar(&bar.s_full[g], (t >> 1) & 1, abort_flag, a.status));
       if (!ok) break;
@@ -504,8 +509,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
       ok = __all_sync(0xffffffffu, wait_bar(&bar.dp_full[g], (t >> 1) & 1, abort_flag, a.status));
       if (!ok) break;
       fence_after();
-      uint32_t pk[32];
       if (need) {
+        uint32_t pk[32];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           float dp[32];
@@ -519,12 +524,9 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
             pk[16 * hh + c] = pack_bf16(d0, d1);
           }
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = 0u;
+        tmem_st32(st + 64, pk);
+        tmem_wait_st();
       }
-      tmem_st32(st + 64, pk);
-      tmem_wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ds_full[g]);
@@ -543,7 +545,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         if (!valid) continue;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          v[e] = T > 0 ? a.scale * v[e] : 0.f;
+          v[e] *= a.scale;
           if (anch) v[e] += da[32 * c + e];
         }
 #pragma unroll
@@ -583,7 +585,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
   const int b = (int)(bh / a.H), h = (int)(bh % a.H);
 
   if (tid == 0) {
-    mbar_init(&bar.own_full, 1);
+    mbar_init(&bar.own_full, 1 + 256);   // the owned tiles' load, and the softmax threads' zeroed accumulators
     for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.s_full[s], 1); mbar_init(&bar.dp_full[s], 1);
@@ -683,28 +685,44 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     uint64_t* ready = first ? bar.p_full : bar.ds_full;
     RingPos<S> ld, use;
     auto wait_ld = [&]() { return wait_bar(&bar.full[ld.s], ld.ph, abort_flag, a.status); };
-    auto start = [&](int g) {
+    auto start = [&](int g, int e) {
+      const uint64_t b0 = sd + ld.s * kStep;
+      ld.next();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss_w(col + 128 * g, kmaj<D>(od, kk, C::kOChunk), kmaj<D>(sd + ld.s * kStep, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u);
+        mma_ss_m(col + 128 * g, kmaj<D>(od, kk, C::kOChunk), kmaj<D>(b0, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u, off(e, 0), off(e, 1));
       mma_commit_w(&done[g]);
-      ld.next();
     };
-    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
-    for (int t = 0; t < 2 && t < T && ok; ++t)
-      if ((ok = __all_sync(0xffffffffu, wait_ld()))) start(t);
-    for (int t = 0; t < T && ok; ++t) {
-      const bool more = t + 2 < T;
-      ok = !more || wait_ld();
-      ok = ok && wait_bar(&ready[t & 1], (t >> 1) & 1, abort_flag, a.status);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      fence_after();
+    auto finish = [&](int t, int e) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_ts_w(acc, col + 128 * (t & 1) + kk * 8, gd + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, (t | kk) ? 1u : 0u);
+        mma_ts_m(acc, col + 128 * (t & 1) + kk * 8, gd + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, 1u, off(e, 0), off(e, 1));
       mma_commit_w(&bar.empty[use.s]);
       use.next();
-      if (more) start(t & 1);
+    };
+    // a step's list entry (its halves); centroid tiles take every row
+    auto entry = [&](int t) { return kCent ? 3 << 16 : x.list[t]; };
+    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
+    fence_after();
+    for (int t = 0; t < 2 && t < T && ok; ++t)
+      if ((ok = __all_sync(0xffffffffu, wait_ld()))) start(t, entry(t));
+    int t = 0, e0 = T > 0 ? entry(0) : 0, e1 = T > 1 ? entry(1) : 0, e2 = T > 2 ? entry(2) : 0;   // steps t, t+1, t+2
+    for (; t < T - 2 && ok; ++t) {   // (no condition around a batch: see the last two steps below)
+      ok = wait_ld() && wait_bar(&ready[t & 1], (t >> 1) & 1, abort_flag, a.status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      fence_after();
+      finish(t, e0);
+      const int e = e2;
+      e0 = e1;
+      e1 = e2;
+      e2 = entry(min(t + 3, T - 1));
+      start(t & 1, e);
+    }
+    for (; t < T && ok; ++t) {
+      if (!(ok = __all_sync(0xffffffffu, wait_bar(&ready[t & 1], (t >> 1) & 1, abort_flag, a.status)))) break;
+      fence_after();
+      finish(t, e0);
+      e0 = e1;
     }
     mma_commit_w(&bar.final_mma);
     if (first) drain_bar(&bar.final_mma, 0, a.status);
@@ -724,6 +742,15 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
           for (int s = 0; s < a.splits; ++s) v += src[((s * bhs + bh) * a.nb + jj) * D + d];
         x.gsum[which][half][d] = v;
       }
+    }
+    {   // accumulators from zero: group 0 dK, group 1 dV
+      uint32_t z[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) z[c] = 0u;
+      for (int c = 0; c < D / 32; ++c) tmem_st32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, z);
+      tmem_wait_st();
+      fence_before();
+      mbar_arrive(&bar.own_full);
     }
     uint64_t gb2 = 0ull;   // kCent: the sums of ds of even and odd queries
     bool ok = true;
@@ -763,12 +790,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
             pk[2 * c + u] = pack_bf16(p[k], p[k + 1]);
           }
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = 0u;
+        tmem_st32(st, pk);
+        tmem_wait_st();
       }
-      tmem_st32(st, pk);
-      tmem_wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full[g]);
@@ -796,9 +820,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
             }
           }
         }
+        tmem_st32(st + 64, pk);
+        tmem_wait_st();
       }
-      tmem_st32(st + 64, pk);
-      tmem_wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ds_full[g]);
@@ -817,7 +841,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         const int64_t at = (split * bhs + bh) * a.nb + j;
         if (g == 1 && store) a.gb_[at] = x.gb[r] + gbs;
         float* dst = (g ? a.gv : a.gk) + at * D;   // group 0 stores gk, group 1 gv
-        const float mul = T > 0 ? (g ? 1.f : a.scale) : 0.f;
+        const float mul = g ? 1.f : a.scale;
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
           __syncwarp();
@@ -826,8 +850,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
           if (!store) continue;
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + 32 * c + e) =
-                T > 0 ? make_float4(mul * v[e], mul * v[e + 1], mul * v[e + 2], mul * v[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(dst + 32 * c + e) = make_float4(mul * v[e], mul * v[e + 1], mul * v[e + 2], mul * v[e + 3]);
         }
       } else {
         const int row = 128 * tk + r;
@@ -850,7 +873,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
           if (!store) continue;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            v[e] = T > 0 ? sc * v[e] : 0.f;
+            v[e] *= sc;
             if (a.centroids) v[e] = fmaf(mul, gs[32 * c + e], v[e]);
             if (a.centroids && a.mode && g == 0) v[e] = fmaf(beta, an[32 * c + e], v[e]);
           }

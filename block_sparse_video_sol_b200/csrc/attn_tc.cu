@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const AttnArgs a,
   // block unselected by a present half: lane w checks word w
   const bool present1 = i0 + 1 < a.nqb;
   const uint32_t vm = lane < mw ? (a.nkb - 32 * lane >= 32 ? 0xffffffffu : ((1u << (a.nkb - 32 * lane)) - 1u)) : 0u;
-  const uint32_t wb = __ballot_sync(0xffffffffu, ((~ua & vm) != 0u) || (present1 && (~ub & vm) != 0u));
+  const uint32_t wa0 = __ballot_sync(0xffffffffu, (~ua & vm) != 0u);
+  const uint32_t wa1 = __ballot_sync(0xffffffffu, present1 && (~ub & vm) != 0u);
+  const uint32_t wb = wa0 | wa1;
   if (lane < mw) {
     P[16 + lane] = (int)ua;
     P[16 + mw + lane] = (int)ub;
@@ -292,6 +294,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const AttnArgs a,
     P[0] = NA + NB + NC;
     P[1] = a.centroids ? n : 0;   // Top-K routing without the compressed branch drops unselected blocks
     P[2] = present1 ? 1 : 0;
+    P[12] = a.centroids ? (int)wa0 : 0;   // bitmap words with a block unselected by the first / second block
+    P[13] = a.centroids ? (int)wa1 : 0;
   }
 }
 

@@ -22,7 +22,8 @@ __device__ __forceinline__ void raise_status(int* status, int code) {
 
 // Ints of one query tile's attention plan (built from the CSR lists before the
 // attention kernel): a 16-int header (union length, centroid tile count,
-// whether the second query block exists, the centroid tiles), both halves'
+// whether the second query block exists, the centroid tiles, at 12 and 13 the
+// bitmap words that leave a block to its centroid), both halves'
 // exact-block bitmaps (mask_words each), then the union list (<= nkb entries).
 __host__ __device__ inline int plan_ints(int mask_words, int nkb) { return (16 + 2 * mask_words + nkb + 3) & ~3; }
 

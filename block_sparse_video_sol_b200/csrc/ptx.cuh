@@ -163,6 +163,20 @@ __device__ __forceinline__ void mma_ts_w(uint32_t d, uint32_t a, uint64_t b, uin
                "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
                :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc));
 }
+// The same with rows left out: where off0 (rows 0-63) or off1 (rows 64-127) is all ones, the
+// accumulator's rows are not updated.
+__device__ __forceinline__ void mma_ss_m(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t off0,
+                                         uint32_t off1) {
+  asm volatile("{ .reg .pred p, e; setp.ne.b32 p, %4, 0; elect.sync _|e, 0xffffffff;\n"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %6, %6}, p; }"
+               :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(off0), "r"(off1));
+}
+__device__ __forceinline__ void mma_ts_m(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t off0,
+                                         uint32_t off1) {
+  asm volatile("{ .reg .pred p, e; setp.ne.b32 p, %4, 0; elect.sync _|e, 0xffffffff;\n"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %6, %6}, p; }"
+               :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc), "r"(off0), "r"(off1));
+}
 __device__ __forceinline__ void mma_commit_w(uint64_t* bar) {
   asm volatile("{ .reg .pred e; elect.sync _|e, 0xffffffff;\n"
                "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }"
