@@ -13,31 +13,46 @@
 //   dx = r (u - x r^2 sum(u x) / D),  dw = sum over rows of g x r.
 //
 // Both are HBM-bound (each input element read once, each output written once).
-// A row is D/8 lanes of 16 bytes; a warp takes one position, one of Q / K and
-// kHeads heads per lane group, whose loads are all in flight together.
+// A row is D/8 lanes of 16 bytes.  A unit is one position of one of Q / K and
+// kHeads heads per lane group of a warp; a warp keeps three or four of its units
+// in flight with 16-byte asynchronous copies into shared memory, each lane reading
+// back only what it copied (no barrier, and no registers held by loads in flight).
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
+#include "ptx.cuh"   // cp.async
 
 namespace sol {
 namespace {
 
-constexpr int kHeads = 4;      // heads in flight per lane group
-constexpr int kFwdWarps = 4;   // warps per CTA (forward)
-constexpr int kBwdWarps = 8;   // warps per CTA (backward)
+constexpr int kHeads = 4;       // heads per lane group of a unit
+constexpr int kWarps = 4;       // warps per CTA
+constexpr int kFwdStages = 4, kBwdStages = 3;   // units in flight per warp
+constexpr int kFew = 3, kFwdMost = 6, kBwdMost = 4;   // CTAs an SM: see make_plan
+constexpr int kSms = 148;
+constexpr int kFwdSmem = kWarps * kFwdStages * kHeads * 512;
+constexpr int kBwdSmem = kWarps * kBwdStages * 2 * kHeads * 512;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
+// Eight bf16 as four fp32 pairs, and back.
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t* f) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = f2pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack2(uint64_t f) {
+  float lo, hi;
+  f2unpack(f, lo, hi);
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t* f) {
+  return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+__device__ __forceinline__ float sum2(uint64_t f) {
+  float lo, hi;
+  f2unpack(f, lo, hi);
+  return lo + hi;
 }
 
 // Eight weights from dim d0 (ones without a weight).
@@ -46,7 +61,10 @@ __device__ __forceinline__ void load_weight(const NormRopeArgs& a, int t, int d0
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = 1.f;
   } else if (a.w_bf16) {
-    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w[t]) + d0), w);
+    uint64_t f[4];
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w[t]) + d0), f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2unpack(f[i], w[2 * i], w[2 * i + 1]);
   } else {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.w[t]) + d0);
     const float4 x = p[0], y = p[1];
@@ -101,14 +119,11 @@ __device__ __forceinline__ void load_turn(const NormRopeArgs& a, int b, int n, i
 // The partners' eight values of this lane's dims (packed bf16), by shuffle for
 // split pairs and by swapping neighbours for interleaved ones.
 template <bool kInter, int LPR>
-__device__ __forceinline__ void partners(const uint4& u, int partner, float* f) {
+__device__ __forceinline__ void partners(const uint4& u, int partner, uint64_t* f) {
   if (kInter) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] & 0xffff0000u);
-      f[2 * i + 1] = __uint_as_float(w[i] << 16);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = f2pack(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(w[i] << 16));
   } else {
     uint4 o;
     o.x = __shfl_sync(0xffffffffu, u.x, partner, LPR);
@@ -119,133 +134,236 @@ __device__ __forceinline__ void partners(const uint4& u, int partner, float* f) 
   }
 }
 
-// Item it of (b, n, head chunk), chunks fastest, so neighbouring warps read neighbouring heads.
-struct Item {
-  int b, n, h0;
+// The work is cut into jobs (t, b, n, part): one of Q / K, one position, one of
+// `parts` runs of its head chunks (kHeads heads per lane group each).  Job w of
+// the W warps' first round is warp w's, and every further one W jobs on, so that
+// all warps read and write in one moving window (ranges of their own, one per
+// warp, spread the accesses over every page of the tensors at once).  The job
+// index is kept in digits and stepped by W's digits: no division per job.
+struct Grid {
+  int chunks, parts, N, B;
 };
-__device__ __forceinline__ Item item_at(const NormRopeArgs& a, int64_t it, int heads) {
-  Item r;
-  const int chunks = (a.H + heads - 1) / heads;
-  r.h0 = (int)(it % chunks) * heads;
-  it /= chunks;
-  r.n = (int)(it % a.N);
-  r.b = (int)(it / a.N);
-  return r;
+struct Pos {
+  int p, n, b, t;      // the job
+  int chunk, end;      // its next head chunk, and where they end
+  int dp, dn, db, dt;  // W in the same digits
+  __device__ __forceinline__ static void digits(int j, const Grid& g, int& p, int& n, int& b, int& t) {
+    p = j % g.parts;
+    j /= g.parts;
+    n = j % g.N;
+    j /= g.N;
+    b = j % g.B;
+    t = j / g.B;
+  }
+  __device__ __forceinline__ Pos(int w, int W, const Grid& g) {
+    digits(w, g, p, n, b, t);
+    digits(W, g, dp, dn, db, dt);
+    open(g);
+  }
+  __device__ __forceinline__ void open(const Grid& g) {
+    chunk = p * g.chunks / g.parts;
+    end = (p + 1) * g.chunks / g.parts;
+  }
+  // to the next head chunk; true at a new job
+  __device__ __forceinline__ bool next(const Grid& g) {
+    if (++chunk < end) return false;
+    p += dp; n += dn; b += db; t += dt;
+    if (p >= g.parts) { p -= g.parts; ++n; }
+    if (n >= g.N) { n -= g.N; ++b; }
+    if (b >= g.B) { b -= g.B; ++t; }
+    open(g);
+    return true;
+  }
+};
+
+template <int D, bool kInter, int kCtas>   // kCtas: CTAs an SM, for which registers are allotted
+__global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const NormRopeArgs a, const Grid gr) {
+  constexpr int LPR = D / 8, GPW = 32 / LPR, kUnitHeads = GPW * kHeads;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LPR, g = lane / LPR;
+  const int w = blockIdx.x * kWarps + warp, W = gridDim.x * kWarps;
+  Pos in(w, W, gr);   // the tensor is the slowest digit: t = 2 is past the last job
+  if (in.t >= 2) return;   // whole warp
+  Pos at = in;
+  uint4* ring = reinterpret_cast<uint4*>(smem) + (warp * kFwdStages * kHeads) * 32 + lane;
+  auto row = [&](const __nv_bfloat16* x, const Pos& p, int64_t sb, int64_t sn, int64_t sh) {
+    return x + (int64_t)p.b * sb + (int64_t)p.n * sn + (int64_t)g * sh + 8 * c;
+  };
+  const __nv_bfloat16* xr = row(a.x[in.t], in, a.sb, a.sn, a.sh);
+  auto fetch = [&](int stage) {
+    if (in.t < 2) {
+      const __nv_bfloat16* x = xr + (int64_t)in.chunk * (kUnitHeads * a.sh);
+#pragma unroll
+      for (int e = 0; e < kHeads; ++e)
+        if (in.chunk * kUnitHeads + GPW * e + g < a.H) cp_async16(ring + (stage * kHeads + e) * 32, x + e * (GPW * a.sh));
+      if (in.next(gr) && in.t < 2) xr = row(a.x[in.t], in, a.sb, a.sn, a.sh);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kFwdStages; ++s) fetch(s);
+  uint64_t A[4], Bp[4];
+  __nv_bfloat16* yr = nullptr;
+  int partner = c, stage = 0;
+  bool fresh = true;   // a new position: its angles and weights
+  while (at.t < 2) {
+    if (fresh) {   // uniform over the warp
+      Turn tr;
+      load_turn<kInter>(a, at.b, at.n, c, tr);
+      float wt[8];
+      load_weight(a, at.t, 8 * c, wt);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) A[e] = f2pack(wt[2 * e] * tr.c[2 * e], wt[2 * e + 1] * tr.c[2 * e + 1]);
+      if (!kInter) load_weight(a, at.t, 8 * tr.partner, wt);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        Bp[e] = f2pack(wt[kInter ? 2 * e + 1 : 2 * e] * tr.s[2 * e], wt[kInter ? 2 * e : 2 * e + 1] * tr.s[2 * e + 1]);
+      partner = tr.partner;
+      yr = const_cast<__nv_bfloat16*>(row(a.y[at.t], at, a.ob, a.on, a.oh));
+    }
+    __nv_bfloat16* y = yr + (int64_t)at.chunk * (kUnitHeads * a.oh);
+    const int h0 = at.chunk * kUnitHeads + g;
+    cp_async_wait<kFwdStages - 1>();
+    uint4 u[kHeads];
+#pragma unroll
+    for (int e = 0; e < kHeads; ++e) u[e] = ring[(stage * kHeads + e) * 32];
+    fetch(stage);
+    stage = stage + 1 == kFwdStages ? 0 : stage + 1;
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      uint64_t f[4], fp[4], s2 = 0ull;
+      unpack8(u[k], f);
+      partners<kInter, LPR>(u[k], partner, fp);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s2 = ffma2(f[e], f[e], s2);
+      float ss = sum2(s2);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(ss * (1.f / D) + a.eps);
+      const uint64_t r2 = f2pack(r, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = fmul2(r2, ffma2(f[e], A[e], fmul2(fp[e], Bp[e])));
+      if (h0 + GPW * k < a.H) *reinterpret_cast<uint4*>(y + k * (GPW * a.oh)) = pack8(f);
+    }
+    fresh = at.next(gr);
+  }
+  cp_async_wait<0>();
 }
 
-template <int D, bool kInter>
-__global__ void __launch_bounds__(kFwdWarps * 32) norm_rope_kernel(const NormRopeArgs a, int64_t items) {
-  constexpr int LPR = D / 8, GPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, c = lane % LPR, g = lane / LPR;
-  const int t = blockIdx.y;   // 0: Q, 1: K
-  const int64_t it = (int64_t)blockIdx.x * kFwdWarps + (threadIdx.x >> 5);
-  if (it >= items) return;    // whole warp
-  const Item m = item_at(a, it, GPW * kHeads);
-  const __nv_bfloat16* x = a.x[t] + (int64_t)m.b * a.sb + (int64_t)m.n * a.sn + 8 * c;
-  __nv_bfloat16* y = a.y[t] + (int64_t)m.b * a.ob + (int64_t)m.n * a.on + 8 * c;
-  uint4 u[kHeads];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = m.h0 + GPW * i + g;
-    u[i] = make_uint4(0, 0, 0, 0);
-    if (h < a.H) u[i] = *reinterpret_cast<const uint4*>(x + (int64_t)h * a.sh);
-  }
-  Turn tr;
-  load_turn<kInter>(a, m.b, m.n, c, tr);
-  float A[8], Bp[8], w[8];
-  load_weight(a, t, 8 * c, w);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) A[i] = w[i] * tr.c[i];
-  if (kInter) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) Bp[i] = w[i ^ 1] * tr.s[i];
-  } else {
-    load_weight(a, t, 8 * tr.partner, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) Bp[i] = w[i] * tr.s[i];
-  }
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = m.h0 + GPW * i + g;
-    float f[8], fp[8], ss = 0.f;
-    unpack8(u[i], f);
-    partners<kInter, LPR>(u[i], tr.partner, fp);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = r * fmaf(f[e], A[e], fp[e] * Bp[e]);
-    if (h < a.H) *reinterpret_cast<uint4*>(y + (int64_t)h * a.oh) = pack8(f);
-  }
-}
-
-// Backward.  The CTAs of one tensor (blockIdx.y) walk its items in a fixed
-// stride, so each lane's weight-gradient sum has a fixed order; the CTA's sums
+// Backward.  The CTAs of one tensor (blockIdx.y) share its jobs in a fixed
+// order, so each lane's weight-gradient sum has one too; the CTA's sums
 // go to part[t][blockIdx.x][D] and dw_kernel adds them in CTA order.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kBwdWarps * 32) norm_rope_bwd_kernel(const NormRopeArgs a, int64_t items) {
-  constexpr int LPR = D / 8, GPW = 32 / LPR;
-  __shared__ float red[kBwdWarps * GPW][D];
+__global__ void __launch_bounds__(kWarps * 32, kBwdMost) norm_rope_bwd_kernel(const NormRopeArgs a, const Grid gr) {
+  constexpr int LPR = D / 8, GPW = 32 / LPR, kUnitHeads = GPW * kHeads;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[kWarps * GPW][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LPR, g = lane / LPR;
   const int t = blockIdx.y;
-  float w[8], dw[8];
-  load_weight(a, t, 8 * c, w);
+  const int wi = blockIdx.x * kWarps + warp, W = gridDim.x * kWarps;
+  Pos in(wi, W, gr);   // one tensor's jobs: t = 1 is past the last
+  Pos at = in;
+  uint4* ring = reinterpret_cast<uint4*>(smem) + (warp * kBwdStages * 2 * kHeads) * 32 + lane;
+  auto row = [&](const __nv_bfloat16* x, const Pos& p, int64_t sb, int64_t sn, int64_t sh) {
+    return x + (int64_t)p.b * sb + (int64_t)p.n * sn + (int64_t)g * sh + 8 * c;
+  };
+  const __nv_bfloat16 *xr = row(a.x[t], in, a.sb, a.sn, a.sh), *zr = row(a.dz[t], in, a.ob, a.on, a.oh);
+  auto fetch = [&](int stage) {
+    if (in.t == 0) {
+      const __nv_bfloat16* x = xr + (int64_t)in.chunk * (kUnitHeads * a.sh);
+      const __nv_bfloat16* z = zr + (int64_t)in.chunk * (kUnitHeads * a.oh);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
-  for (int64_t it = (int64_t)blockIdx.x * kBwdWarps + warp; it < items; it += (int64_t)gridDim.x * kBwdWarps) {
-    const Item m = item_at(a, it, GPW * kHeads);
-    const __nv_bfloat16* x = a.x[t] + (int64_t)m.b * a.sb + (int64_t)m.n * a.sn + 8 * c;
-    const __nv_bfloat16* dz = a.dz[t] + (int64_t)m.b * a.ob + (int64_t)m.n * a.on + 8 * c;
-    __nv_bfloat16* dx = a.y[t] + (int64_t)m.b * a.gb + (int64_t)m.n * a.gn + 8 * c;
-    uint4 u[kHeads], v[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      const int h = m.h0 + GPW * i + g;
-      u[i] = v[i] = make_uint4(0, 0, 0, 0);
-      if (h < a.H) {
-        u[i] = *reinterpret_cast<const uint4*>(x + (int64_t)h * a.sh);
-        v[i] = *reinterpret_cast<const uint4*>(dz + (int64_t)h * a.oh);
+      for (int e = 0; e < kHeads; ++e)
+        if (in.chunk * kUnitHeads + GPW * e + g < a.H) {
+          cp_async16(ring + (stage * 2 * kHeads + 2 * e) * 32, x + e * (GPW * a.sh));
+          cp_async16(ring + (stage * 2 * kHeads + 2 * e + 1) * 32, z + e * (GPW * a.oh));
+        }
+      if (in.next(gr) && in.t == 0) {
+        xr = row(a.x[t], in, a.sb, a.sn, a.sh);
+        zr = row(a.dz[t], in, a.ob, a.on, a.oh);
       }
     }
-    Turn tr;
-    load_turn<kInter>(a, m.b, m.n, c, tr);
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      const int h = m.h0 + GPW * i + g;
-      float f[8], z[8], zp[8], ss = 0.f, sx = 0.f;
-      unpack8(u[i], f);
-      unpack8(v[i], z);
-      partners<kInter, LPR>(v[i], tr.partner, zp);
+  for (int s = 0; s < kBwdStages; ++s) fetch(s);
+  uint64_t w[4], dw[4], cs[4], sn[4];
+  {
+    float wt[8];
+    load_weight(a, t, 8 * c, wt);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        z[e] = fmaf(z[e], tr.c[e], -(zp[e] * tr.s[e]));   // g = R^T dz
-        ss = fmaf(f[e], f[e], ss);
-        sx = fmaf(w[e] * z[e], f[e], sx);
+    for (int i = 0; i < 4; ++i) { w[i] = f2pack(wt[2 * i], wt[2 * i + 1]); dw[i] = 0ull; cs[i] = sn[i] = 0ull; }
+  }
+  __nv_bfloat16* dxr = nullptr;
+  int partner = c, stage = 0;
+  bool fresh = true;
+  while (at.t == 0) {
+    if (fresh) {   // uniform over the warp
+      Turn tr;
+      load_turn<kInter>(a, at.b, at.n, c, tr);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        cs[e] = f2pack(tr.c[2 * e], tr.c[2 * e + 1]);
+        sn[e] = f2pack(-tr.s[2 * e], -tr.s[2 * e + 1]);   // the turn back
       }
+      partner = tr.partner;
+      dxr = const_cast<__nv_bfloat16*>(row(a.y[t], at, a.gb, a.gn, a.gh));
+    }
+    __nv_bfloat16* dx = dxr + (int64_t)at.chunk * (kUnitHeads * a.gh);
+    const int h0 = at.chunk * kUnitHeads + g;
+    cp_async_wait<kBwdStages - 1>();
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const bool live = h0 + GPW * k < a.H;
+      uint64_t f[4], z[4], zp[4], ss2 = 0ull, sx2 = 0ull;
+      uint4 u = make_uint4(0, 0, 0, 0), v = u;
+      if (live) {
+        u = ring[(stage * 2 * kHeads + 2 * k) * 32];
+        v = ring[(stage * 2 * kHeads + 2 * k + 1) * 32];
+      }
+      unpack8(u, f);
+      unpack8(v, z);
+      partners<kInter, LPR>(v, partner, zp);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[e] = ffma2(z[e], cs[e], fmul2(zp[e], sn[e]));   // g = R^T dz
+        ss2 = ffma2(f[e], f[e], ss2);
+        zp[e] = fmul2(w[e], z[e]);                        // u = w g
+        sx2 = ffma2(zp[e], f[e], sx2);
+      }
+      float ss = sum2(ss2), sx = sum2(sx2);
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) {
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
         sx += __shfl_xor_sync(0xffffffffu, sx, o);
       }
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const float k = r * r * sx * (1.f / D);
+      const float q = -r * r * sx * (1.f / D);
+      const uint64_t r2 = f2pack(r, r), q2 = f2pack(q, q);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dw[e] = fmaf(z[e] * r, f[e], dw[e]);
-        z[e] = r * fmaf(-k, f[e], w[e] * z[e]);
+      for (int e = 0; e < 4; ++e) {
+        dw[e] = ffma2(fmul2(z[e], r2), f[e], dw[e]);
+        z[e] = fmul2(r2, ffma2(q2, f[e], zp[e]));
       }
-      if (h < a.H) *reinterpret_cast<uint4*>(dx + (int64_t)h * a.gh) = pack8(z);
+      if (live) *reinterpret_cast<uint4*>(dx + k * (GPW * a.gh)) = pack8(z);
     }
+    fetch(stage);
+    stage = stage + 1 == kBwdStages ? 0 : stage + 1;
+    fresh = at.next(gr);
   }
+  cp_async_wait<0>();
   if (!a.dw[t]) return;   // uniform over the CTA
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[warp * GPW + g][8 * c + i] = dw[i];
+  for (int i = 0; i < 4; ++i) {
+    float lo2, hi2;
+    f2unpack(dw[i], lo2, hi2);
+    red[warp * GPW + g][8 * c + 2 * i] = lo2;
+    red[warp * GPW + g][8 * c + 2 * i + 1] = hi2;
+  }
   __syncthreads();
   if (threadIdx.x < D) {
     float s = 0.f;
-    for (int i = 0; i < kBwdWarps * GPW; ++i) s += red[i][threadIdx.x];
+    for (int i = 0; i < kWarps * GPW; ++i) s += red[i][threadIdx.x];
     a.dw_part[((int64_t)t * gridDim.x + blockIdx.x) * D + threadIdx.x] = s;
   }
 }
@@ -270,38 +388,69 @@ __global__ void __launch_bounds__(1024) dw_kernel(const NormRopeArgs a, int part
   }
 }
 
-int64_t item_count(const NormRopeArgs& a, int D) {
-  const int heads = 32 / (D / 8) * kHeads;
-  return (int64_t)a.B * a.N * ((a.H + heads - 1) / heads);
+// The jobs of `tensors` tensors and the CTAs for them (a tensor's share of `most`
+// an SM).  Twelve warps an SM carry the copy rate where a position has several
+// head chunks, and more lose some of it (N = 32768, H = 56, D = 128: forward 300 us
+// with 12 warps, 343 with 16, 360 with 24; backward 437 / 493 us with 12 / 16).  With
+// few heads a position's angles are most of the work and more warps win (H = 8:
+// forward 82 us with 12 warps, 66 with 24, backward 103 / 90 us with 12 / 16; the
+// two meet at 32 heads of 128 dims, four chunks).  A job is a whole position where every warp
+// gets several, else a single head chunk (short calls: more warps at work).
+struct Plan {
+  Grid g;
+  int ctas;
+  bool few;
+};
+Plan make_plan(int B, int N, int H, int D, int tensors, int most) {
+  const int heads = 32 / (D / 8) * kHeads, chunks = (H + heads - 1) / heads;
+  const bool few = chunks >= 5;
+  const int room = kSms * (few ? kFew : most) * tensors / 2;
+  Plan r{Grid{chunks, 1, N, B}, 0, few};
+  const int64_t positions = (int64_t)tensors * B * N;
+  if (positions < 4 * (int64_t)room * kWarps) r.g.parts = chunks;
+  r.ctas = (int)std::min<int64_t>((positions * r.g.parts + kWarps - 1) / kWarps, room);
+  return r;
+}
+
+// Once per device: opt in to the shared memory.
+template <int D, bool kInter>
+cudaError_t prepare() {
+  static std::atomic<int> done[64];   // zero-initialised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
+  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(norm_rope_kernel<D, kInter, kFew>, at, kFwdSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(norm_rope_kernel<D, kInter, kFwdMost>, at, kFwdSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D, kInter>, at, kBwdSmem)) != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_release);
+  return cudaSuccess;
 }
 
 template <int D, bool kInter>
 cudaError_t fwd(const NormRopeArgs& a, cudaStream_t st) {
-  const int64_t items = item_count(a, D);
-  const dim3 grid((unsigned)((items + kFwdWarps - 1) / kFwdWarps), 2);
-  norm_rope_kernel<D, kInter><<<grid, kFwdWarps * 32, 0, st>>>(a, items);
+  cudaError_t e = prepare<D, kInter>();
+  if (e != cudaSuccess) return e;
+  const Plan r = make_plan(a.B, a.N, a.H, D, 2, kFwdMost);
+  if (r.few) norm_rope_kernel<D, kInter, kFew><<<r.ctas, kWarps * 32, kFwdSmem, st>>>(a, r.g);
+  else norm_rope_kernel<D, kInter, kFwdMost><<<r.ctas, kWarps * 32, kFwdSmem, st>>>(a, r.g);
   return cudaGetLastError();
 }
 
 template <int D, bool kInter>
 cudaError_t bwd(const NormRopeArgs& a, cudaStream_t st) {
-  const int64_t items = item_count(a, D);
-  const int parts = norm_rope_parts(a.B, a.N, a.H, D);
-  norm_rope_bwd_kernel<D, kInter><<<dim3(parts, 2), kBwdWarps * 32, 0, st>>>(a, items);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || (!a.dw[0] && !a.dw[1])) return e;
-  dw_kernel<D><<<2, 1024, 0, st>>>(a, parts);
+  cudaError_t e = prepare<D, kInter>();
+  if (e != cudaSuccess) return e;
+  const Plan r = make_plan(a.B, a.N, a.H, D, 1, kBwdMost);
+  norm_rope_bwd_kernel<D, kInter><<<dim3(r.ctas, 2), kWarps * 32, kBwdSmem, st>>>(a, r.g);
+  if ((e = cudaGetLastError()) != cudaSuccess || (!a.dw[0] && !a.dw[1])) return e;
+  dw_kernel<D><<<2, 1024, 0, st>>>(a, r.ctas);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int norm_rope_parts(int B, int N, int H, int D) {
-  const int heads = 32 / (D / 8) * kHeads;
-  const int64_t items = (int64_t)B * N * ((H + heads - 1) / heads);
-  const int64_t ctas = (items + kBwdWarps - 1) / kBwdWarps;
-  return (int)(ctas < 2 * 148 ? ctas : 2 * 148);   // two tensors: four CTAs an SM
-}
+int norm_rope_parts(int B, int N, int H, int D) { return make_plan(B, N, H, D, 1, kBwdMost).ctas; }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int D, cudaStream_t st) {
   if (D == 128) return a.inter ? fwd<128, true>(a, st) : fwd<128, false>(a, st);

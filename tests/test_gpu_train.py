@@ -279,6 +279,37 @@ def test_norm_rope_forward_and_backward(sol, B, N, H, weights, tables_b, inter, 
         assert (np.abs(g.cpu().numpy() - ew) <= 2.0 ** -24 * 600 * mag + 1e-30).all()
 
 
+@pytest.mark.parametrize("N,H,D", [(4100, 40, 128), (5003, 90, 64), (16500, 3, 128)])
+def test_norm_rope_long(sol, N, H, D):
+    """Lengths at which a warp takes several whole positions; every row checked in fp64 on the GPU."""
+    B, rot = 1, D
+    q, k, w, cos, sin, dqo, dko = rope_inputs(B, N, H, D, rot, torch.float32, 0, N)
+    p = sol.make_params(B, N, H, D)
+    nr = sol.make_norm_rope(*w, cos, sin, 1e-6)
+    qo, ko, dq, dk = (torch.full_like(q, float("nan")) for _ in range(4))
+    dw = [torch.full((D,), float("nan"), device="cuda") for _ in range(2)]
+    ws = torch.full((sol.sol_qk_norm_rope_bwd_workspace_bytes(p),), 255, dtype=torch.uint8, device="cuda")
+    sol.sol_qk_norm_rope(p, nr, q, k, qo, ko)
+    sol.sol_qk_norm_rope_bwd(p, nr, q, k, dqo, dko, dq, dk, *dw, ws)
+    c, s = torch.cat([cos, cos], -1).double()[None, :, None], torch.cat([-sin, sin], -1).double()[None, :, None]
+    swap = lambda t: torch.cat([t[..., D // 2:], t[..., :D // 2]], -1)
+    for x, wt, y, dz, dx, g in ((q, w[0], qo, dqo, dq, dw[0]), (k, w[1], ko, dko, dk, dw[1])):
+        x, z, wt = x.double(), dz.double(), wt.double()
+        r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6)
+        n = x * r * wt
+        want = n * c + swap(n) * s
+        size = (n * c).abs() + (swap(n) * s).abs()
+        assert ((y.double() - want).abs() <= U * want.abs() + 2.0 ** -18 * size + 1e-30).all()
+        gr = z * c - swap(z) * s
+        u = gr * wt
+        ex = r * (u - x * r * r * (u * x).mean(-1, keepdim=True))
+        big = z.norm(dim=-1, keepdim=True) * wt.max() * r * (1 + x.abs() * r)
+        assert ((dx.double() - ex).abs() <= U * ex.abs() + 2.0 ** -18 * big + 1e-30).all()
+        t = gr * x * r
+        # chains of at most N H / 888 + 300 additions
+        assert ((g.double() - t.sum((0, 1, 2))).abs() <= 2.0 ** -24 * (N * H / 888 + 300) * t.abs().sum((0, 1, 2))).all()
+
+
 def test_norm_rope_in_place_strided_and_null_weight_gradients(sol):
     B, N, H, D = 2, 300, 5, 128
     q, k, w, cos, sin, dqo, dko = rope_inputs(B, N, H, D, 128, torch.float32, 0, 1)
