@@ -198,6 +198,7 @@ struct Bars {
   uint64_t full[5], empty[5];       // ring of streamed tile pairs
   uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
   uint64_t p_full[2], ds_full[2];   // S is read (dq) or P is in its place (dkv) / dS is in dP's place
+  uint64_t own_tile;                // dq: Q and dO are in shared memory, on their way to TMEM
   uint64_t cent_ready;              // dq: the centroids' offsets are in shared memory
   uint64_t final_mma;
 };
@@ -255,13 +256,38 @@ __device__ __forceinline__ uint64_t kmaj(uint64_t base, int kk, int chunk) {
   return base + (uint64_t)(((kk >> 2) * chunk + (kk & 3) * 32) >> 4);
 }
 
+// Row r's 32 values of columns 32c .. 32c+31, as bf16, into a SW128 tile of 128 rows
+// (64-column chunks), the layout of the tile stores.
+template <int D>
+__device__ __forceinline__ void put_row(uint8_t* tile, int r, int c, const float* v) {
+  uint8_t* row = tile + (c >> 1) * Cfg<D>::kOChunk + r * 128;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int at = 4 * (c & 1) + u;
+    *reinterpret_cast<uint4*>(row + ((at ^ (r & 7)) << 4)) =
+        make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
+                   pack_bf16(v[8 * u + 4], v[8 * u + 5]), pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+  }
+}
+// The same tile's halves to rows row0 .. row0 + 127 of a BTHD tensor (one thread).
+template <int D>
+__device__ __forceinline__ void store_rows(const CUtensorMap* m, const uint8_t* tile, int row0, int h, int b, int N) {
+  for (int hf = 0; hf < 2; ++hf)
+    if (row0 + 64 * hf < N)
+      for (int c = 0; c < Cfg<D>::kChunks; ++c)
+        tma_store_4d(m, c * 64, h, row0 + 64 * hf, b, tile + c * Cfg<D>::kOChunk + hf * (Cfg<D>::kOChunk / 2));
+  tma_store_wait();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo, const __grid_constant__ CUtensorMap mdq,
+          const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
           const __grid_constant__ CUtensorMap mkb, const __grid_constant__ CUtensorMap mvb, const BwdArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* own = ring + (C::kDqStages - 2) * 2 * C::kSTile;   // Q, dO at the start; the ring's last two stages after
   DqExtra& x = *reinterpret_cast<DqExtra*>(ring + C::kDqStages * 2 * C::kSTile);
   Bars& bar = x.bar;
   volatile int* abort_flag = &x.abort_flag;
@@ -273,6 +299,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
 
   if (tid == 0) {
     mbar_init(&bar.own_full, 256);
+    mbar_init(&bar.own_tile, 1);
     mbar_init(&bar.cent_ready, 1);
     for (int s = 0; s < C::kDqStages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
@@ -282,6 +309,14 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     mbar_init(&bar.final_mma, 2);
     x.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // Q and dO rest in the ring's last two stages until the softmax threads have them
+    // in TMEM (row-per-thread global loads instead held up the plan's by 3,000 clocks)
+    mbar_expect_tx(&bar.own_tile, 2 * C::kOTile);
+    for (int c = 0; c < C::kChunks; ++c)
+      for (int hf = 0; hf < 2; ++hf) {
+        tma_load_4d(own + c * C::kOChunk + hf * (C::kOChunk / 2), &mq, c * 64, h, 64 * (i0 + hf), b, &bar.own_tile);
+        tma_load_4d(own + C::kOTile + c * C::kOChunk + hf * (C::kOChunk / 2), &mdo, c * 64, h, 64 * (i0 + hf), b, &bar.own_tile);
+      }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&x.tmem_base)), "r"(512));
@@ -289,19 +324,6 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
   }
   const int n_tail = a.N - 64 * (a.nb - 1);
   if (tid < 64) x.tail_add[tid] = tid < n_tail ? 0.f : -INFINITY;
-  // The softmax threads' rows of Q (group 0) and dO (group 1), loaded now so that
-  // they arrive beside the plan (rows past N as zeros).
-  const int row = 64 * i0 + (tid & 127);
-  uint4 rows[D / 8];
-  if (warp >= 4) {
-    const __nv_bfloat16* src = warp < 8 ? a.q + (int64_t)b * a.sb + (int64_t)row * a.sn + (int64_t)h * a.sh
-                                        : a.d_o + (int64_t)b * a.ob + (int64_t)row * a.on + (int64_t)h * a.oh;
-#pragma unroll
-    for (int u = 0; u < D / 8; ++u) {
-      rows[u] = make_uint4(0, 0, 0, 0);
-      if (row < a.N) rows[u] = reinterpret_cast<const uint4*>(src)[u];
-    }
-  }
   {
     const int* P = a.plan + (bh * ntq + tq) * plan_ints(mw, a.nb);
     for (int e = tid; e < 2 * mw + a.nb; e += kThreads) {
@@ -329,6 +351,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
       for (int t = 0; t < T; ++t) {
         const int s = t % C::kDqStages, n = t / C::kDqStages;
         if (!wait_bar(&bar.empty[s], (n & 1) ^ 1, abort_flag, a.status)) break;
+        if (t == C::kDqStages - 2 && !wait_bar(&bar.own_full, 0, abort_flag, a.status)) break;
         uint8_t* dst = ring + s * 2 * C::kSTile;
         ++nl;
         mbar_expect_tx(&bar.full[s], 2 * C::kSTile);
@@ -346,6 +369,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         const int cnt = (nl + C::kDqStages - 1 - s) / C::kDqStages;
         if (cnt) drain_bar(&bar.full[s], (cnt - 1) & 1, a.status);
       }
+      drain_bar(&bar.own_tile, 0, a.status);
     }
   } else if (warp == 1 || warp == 2) {
     constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
@@ -438,7 +462,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     if (lane == 0) mbar_arrive(&bar.cent_ready);
   } else if (warp >= 4) {
     const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
-    const bool valid = row < a.N;
+    const int row = 64 * i0 + r;
+    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_tile, 0, abort_flag, a.status));
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
     {   // group 0 puts Q, group 1 dO into TMEM
 #pragma unroll
@@ -446,7 +471,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         uint32_t w[32];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const uint4 v = rows[8 * c + u];
+          const uint4 v = *reinterpret_cast<const uint4*>(own + g * C::kOTile + c * C::kOChunk + r * 128 + ((u ^ (r & 7)) << 4));
           w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
         }
         tmem_st32(lane_addr + (g == 0 ? C::kQ : C::kDo) + 32 * c, w);
@@ -455,6 +480,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
         tmem_st32(lane_addr + C::kDq + g * (D / 2) + 32 * c, w);   // dQ starts from zero (its half)
       }
       tmem_wait_st();
+      fence_async();   // the rows are read before the ring's loads overwrite them
       fence_before();
       mbar_arrive(&bar.own_full);
     }
@@ -463,7 +489,6 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
     const float nd = in_range ? a.ndelta[bh * 64 * a.nb + row] : 0.f;
     const float sl2 = a.scale * kLog2e;
     const uint64_t sl22 = f2pack(sl2, sl2), nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
-    bool ok = true;
     for (int t = g; t < T && ok; t += 2) {
       const float* add = nullptr;
       const int e = entry(t);
@@ -532,29 +557,31 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
       if (lane == 0) mbar_arrive(&bar.ds_full[g]);
     }
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
-    if (ok && !*abort_flag) {
+    __syncwarp();
+    if (ok) {
       fence_after();
       const bool anch = a.da && (row >= a.prefix || a.prefix == a.N);
-      __nv_bfloat16* dst = a.dq + (int64_t)b * a.gb + (int64_t)row * a.gn + (int64_t)h * a.gh;
-      const float* da = a.da + bh * D;
+      const float4* da = reinterpret_cast<const float4*>(a.da + bh * D);
       for (int c = g; c < D / 32; c += 2) {
         float v[32];
         __syncwarp();
         tmem_ld32(lane_addr + C::kDq + 32 * c, v);
         tmem_wait_ld();
-        if (!valid) continue;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] *= a.scale;
-          if (anch) v[e] += da[32 * c + e];
+        for (int e = 0; e < 32; ++e) v[e] *= a.scale;
+        if (anch) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 d = da[8 * c + e];
+            v[4 * e] += d.x; v[4 * e + 1] += d.y; v[4 * e + 2] += d.z; v[4 * e + 3] += d.w;
+          }
         }
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(dst + 32 * c + e) =
-              make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
-                         pack_bf16(v[e + 6], v[e + 7]));
+        put_row<D>(ring, r, c, v);   // the ring is idle: every step is complete
       }
+      fence_async();
     }
+    bar_sync(1, 256);
+    if (tid == 128 && ok && !*abort_flag) store_rows<D>(&mdq, ring, 64 * i0, h, b, a.N);
   }
   fence_before();
   cta_sync();
@@ -567,7 +594,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtens
 template <int D, bool kCent>
 __global__ void __launch_bounds__(kThreads, 1)
 dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo,
-           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const BwdArgs a) {
+           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+           const __grid_constant__ CUtensorMap mgk, const __grid_constant__ CUtensorMap mgv, const BwdArgs a) {
   using C = Cfg<D>;
   constexpr int S = C::kKvStages;
   extern __shared__ uint8_t smem_raw[];
@@ -585,6 +613,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
   const int b = (int)(bh / a.H), h = (int)(bh % a.H);
 
   if (tid == 0) {
+    mbar_init(&bar.cent_ready, 1);
     mbar_init(&bar.own_full, 1 + 256);   // the owned tiles' load, and the softmax threads' zeroed accumulators
     for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
     for (int s = 0; s < 2; ++s) {
@@ -726,6 +755,26 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     }
     mma_commit_w(&bar.final_mma);
     if (first) drain_bar(&bar.final_mma, 0, a.status);
+  } else if (!kCent && warp == 3) {
+    // the two blocks' centroid gradients, summed over the query ranges in order (read after the last step)
+    if (a.centroids) {
+#pragma unroll
+      for (int e = lane; e < D; e += 32) {   // float4s of [gk, gv][half][D]
+        const int d = e % (D / 4), half = (e / (D / 4)) & 1, which = e / (D / 2), jj = 2 * tk + half;
+        const float4* src = reinterpret_cast<const float4*>((which ? a.gv : a.gk) + (bh * a.nb + jj) * D) + d;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (jj < a.nb) {
+#pragma unroll 8
+          for (int s = 0; s < a.splits; ++s) {
+            const float4 u = src[s * bhs * a.nb * (D / 4)];
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+          }
+        }
+        reinterpret_cast<float4*>(x.gsum[which][half])[d] = v;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.cent_ready);
   } else if (warp >= 4) {
     const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
@@ -733,16 +782,6 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     const uint64_t sl22 = f2pack(sl2, sl2);
     const int j = kCent ? 128 * tk + r : 2 * tk + hf;   // this row's centroid / key block
     const float cadd = kCent && j < a.nb ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
-    if (!kCent && a.centroids) {   // the two blocks' centroid gradients, summed over the query ranges in order
-      for (int e = tid - 128; e < 4 * D; e += 256) {
-        const int d = e % D, half = (e / D) & 1, which = e / (2 * D), jj = 2 * tk + half;
-        const float* src = which ? a.gv : a.gk;
-        float v = 0.f;
-        if (jj < a.nb)
-          for (int s = 0; s < a.splits; ++s) v += src[((s * bhs + bh) * a.nb + jj) * D + d];
-        x.gsum[which][half][d] = v;
-      }
-    }
     {   // accumulators from zero: group 0 dK, group 1 dV
       uint32_t z[32];
 #pragma unroll
@@ -832,57 +871,73 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     gbs += gb_odd;
     if (kCent && g == 0) x.gb[r] = gbs;
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
+    if (!kCent && ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.cent_ready, 0, abort_flag, a.status));
     __syncwarp();
-    bar_sync(1, 256);
-    if (ok && !*abort_flag) {
+    if (kCent) bar_sync(1, 256);   // x.gb
+    // Group 0 brings out dk (gk), group 1 dv (gv), through the shared memory that the
+    // tiles no longer need and tile stores.
+    const float sc = g ? 1.f : a.scale;
+    if (ok) {
       fence_after();
       if (kCent) {
-        const bool store = j < a.nb;
-        const int64_t at = (split * bhs + bh) * a.nb + j;
-        if (g == 1 && store) a.gb_[at] = x.gb[r] + gbs;
-        float* dst = (g ? a.gv : a.gk) + at * D;   // group 0 stores gk, group 1 gv
-        const float mul = g ? 1.f : a.scale;
+        if (g == 1 && j < a.nb) a.gb_[(split * bhs + bh) * a.nb + j] = x.gb[r] + gbs;
+        uint8_t* tile = own + g * (128 * D * 4);
+        for (int c = 0; c < D / 32; ++c) {   // fp32 rows: 32-column chunks of 128 bytes, SW128
+          float v[32];
+          __syncwarp();
+          tmem_ld32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<float4*>(tile + c * C::kOChunk + r * 128 + ((u ^ (r & 7)) << 4)) =
+                make_float4(sc * v[4 * u], sc * v[4 * u + 1], sc * v[4 * u + 2], sc * v[4 * u + 3]);
+        }
+      } else {
+        const int row = 128 * tk + r;
+        const int64_t plane = bhs * 64 * a.nb, cr = bh * 64 * a.nb + row;
+        float mul = 0.f, beta = 0.f;   // the row's share of its centroid's gradient, and of the anchor's
+        if (row < a.N && a.centroids) {
+          mul = a.mode ? a.coef[(g ? 2 : 0) * plane + cr] : 1.f / (float)min(64, a.N - 64 * j);
+          if (a.mode && g == 0) beta = a.coef[plane + cr];
+        }
+        const float4* an = reinterpret_cast<const float4*>(a.anchor + bh * D);
+        const float4* gs = reinterpret_cast<const float4*>(x.gsum[g][hf]);
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
           __syncwarp();
           tmem_ld32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, v);
           tmem_wait_ld();
-          if (!store) continue;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(dst + 32 * c + e) = make_float4(mul * v[e], mul * v[e + 1], mul * v[e + 2], mul * v[e + 3]);
-        }
-      } else {
-        const int row = 128 * tk + r;
-        const bool store = row < a.N;
-        const int64_t plane = bhs * 64 * a.nb, cr = bh * 64 * a.nb + row;
-        float mul = 0.f, beta = 0.f;   // the row's share of its centroid's gradient, and of the anchor's
-        if (store && a.centroids) {
-          mul = a.mode ? a.coef[(g ? 2 : 0) * plane + cr] : 1.f / (float)min(64, a.N - 64 * j);
-          if (a.mode && g == 0) beta = a.coef[plane + cr];
-        }
-        const float* an = a.anchor + bh * D;
-        const float* gs = x.gsum[g][hf];
-        __nv_bfloat16* dst = (g ? a.dv : a.dk) + (int64_t)b * a.gb + (int64_t)row * a.gn + (int64_t)h * a.gh;
-        const float sc = g ? 1.f : a.scale;
-        for (int c = 0; c < D / 32; ++c) {   // group 0 stores dk, group 1 dv
-          float v[32];
-          __syncwarp();
-          tmem_ld32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, v);
-          tmem_wait_ld();
-          if (!store) continue;
+          for (int e = 0; e < 32; ++e) v[e] *= sc;
+          if (a.centroids) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            v[e] *= sc;
-            if (a.centroids) v[e] = fmaf(mul, gs[32 * c + e], v[e]);
-            if (a.centroids && a.mode && g == 0) v[e] = fmaf(beta, an[32 * c + e], v[e]);
+            for (int e = 0; e < 8; ++e) {
+              const float4 u = gs[8 * c + e];
+              v[4 * e] = fmaf(mul, u.x, v[4 * e]); v[4 * e + 1] = fmaf(mul, u.y, v[4 * e + 1]);
+              v[4 * e + 2] = fmaf(mul, u.z, v[4 * e + 2]); v[4 * e + 3] = fmaf(mul, u.w, v[4 * e + 3]);
+            }
+            if (a.mode && g == 0) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 u = an[8 * c + e];
+                v[4 * e] = fmaf(beta, u.x, v[4 * e]); v[4 * e + 1] = fmaf(beta, u.y, v[4 * e + 1]);
+                v[4 * e + 2] = fmaf(beta, u.z, v[4 * e + 2]); v[4 * e + 3] = fmaf(beta, u.w, v[4 * e + 3]);
+              }
+            }
           }
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(dst + 32 * c + e) =
-                make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
-                           pack_bf16(v[e + 6], v[e + 7]));
+          put_row<D>(own + g * C::kOTile, r, c, v);
         }
+      }
+      fence_async();
+    }
+    bar_sync(2 + g, 128);
+    if ((tid & 127) == 0 && ok && !*abort_flag) {
+      if (kCent) {
+        for (int c = 0; c < D / 32; ++c)
+          tma_store_3d(g ? &mgv : &mgk, 32 * c, 128 * tk, (int)(split * bhs + bh), own + g * (128 * D * 4) + c * C::kOChunk);
+        tma_store_wait();
+      } else {
+        store_rows<D>(g ? &mgv : &mgk, own + g * C::kOTile, 128 * tk, h, b, a.N);
       }
     }
   }
@@ -1027,6 +1082,7 @@ template <int D>
 constexpr size_t dkv_smem() {
   return 1024 + 2 * Cfg<D>::kOTile + Cfg<D>::kKvStages * 2 * Cfg<D>::kSTile + sizeof(KvExtra<Cfg<D>::kKvStages>);
 }
+static_assert(2 * 128 * 128 * 4 <= 2 * Cfg<128>::kOTile + Cfg<128>::kKvStages * 2 * Cfg<128>::kSTile, "fp32 tiles");
 static_assert(dq_smem<128>() <= 232448 && dkv_smem<128>() <= 232448, "shared memory");
 
 // Once per device (so that launches stay free of attribute calls, e.g. inside a
@@ -1059,13 +1115,22 @@ bool map_cent(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D) {
   const cuuint32_t box[3] = {64, 64, 1};
   return make_map(m, p, 3, dims, str, box, kSw128);
 }
+// 128-row boxes of the centroid gradients' partial sums, fp32 [splits * BH, nb, D].
+bool map_part(CUtensorMap* m, const float* p, const BwdArgs& a, int D) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.nb, (cuuint64_t)a.splits * a.B * a.H};
+  const cuuint64_t str[2] = {(cuuint64_t)D * 4, (cuuint64_t)a.nb * D * 4};
+  const cuuint32_t box[3] = {32, 128, 1};
+  return make_map(m, p, 3, dims, str, box, kSw128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+}
 
 template <int D>
 cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mdo, mkb, mvb;
+  CUtensorMap mq, mk, mv, mdo, mkb, mvb, mdq, mdk, mdv, mgk, mgv;
   if (!map_rows(&mq, a.q, a, D, a.sb, a.sn, a.sh) || !map_rows(&mk, a.k, a, D, a.sb, a.sn, a.sh) ||
       !map_rows(&mv, a.v, a, D, a.sb, a.sn, a.sh) || !map_rows(&mdo, a.d_o, a, D, a.ob, a.on, a.oh) ||
-      !map_cent(&mkb, a.kbar16, a, D) || !map_cent(&mvb, a.vbar16, a, D))
+      !map_cent(&mkb, a.kbar16, a, D) || !map_cent(&mvb, a.vbar16, a, D) || !map_rows(&mdq, a.dq, a, D, a.gb, a.gn, a.gh) ||
+      !map_rows(&mdk, a.dk, a, D, a.gb, a.gn, a.gh) || !map_rows(&mdv, a.dv, a, D, a.gb, a.gn, a.gh) ||
+      (a.centroids && (!map_part(&mgk, a.gk, a, D) || !map_part(&mgv, a.gv, a, D))))
     return cudaErrorInvalidValue;
   cudaError_t e = prepare<D>();
   if (e != cudaSuccess) return e;
@@ -1079,7 +1144,7 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const unsigned bh = (unsigned)(a.B * a.H), tiles = bh * ((a.nb + 1) / 2);
   if (a.centroids) {
-    dkv_kernel<D, true><<<bh * ((a.nb + 127) / 128) * a.splits, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mkb, mvb, a);
+    dkv_kernel<D, true><<<bh * ((a.nb + 127) / 128) * a.splits, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mkb, mvb, mgk, mgv, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (a.centroids && a.mode) {
@@ -1088,9 +1153,9 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
     anchor_bwd_kernel<D><<<a.B * a.H, 1024, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  dq_kernel<D><<<tiles, kThreads, dq_smem<D>(), st>>>(mk, mv, mkb, mvb, a);
+  dq_kernel<D><<<tiles, kThreads, dq_smem<D>(), st>>>(mq, mdo, mdq, mk, mv, mkb, mvb, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  dkv_kernel<D, false><<<tiles, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mk, mv, a);
+  dkv_kernel<D, false><<<tiles, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mk, mv, mdk, mdv, a);
   return cudaGetLastError();
 }
 
