@@ -423,7 +423,7 @@ namespace {
 
 struct BwdLayout {
   int splits;
-  size_t nlse, ndelta, plan, tplan, gk, gv, gb, coef, da_part, da, total;
+  size_t nlse, ndelta, plan, tplan, gk, gv, gb, coef, da_part, da, counter, total;
 };
 BwdLayout bwd_layout(const sol_params& p) {
   BwdLayout R{};
@@ -443,6 +443,7 @@ BwdLayout bwd_layout(const sol_params& p) {
   R.coef = take(pooled * 3 * bh * nb * kBlock * 4);
   R.da_part = take(pooled * bh * nb * p.D * 4);
   R.da = take(pooled * bh * p.D * 4);
+  R.counter = take(4 * 4);
   R.total = off;
   return R;
 }
@@ -554,6 +555,7 @@ sol_status sol_attn_bwd(const sol_params* p, const void* q, const void* k, const
   a.gk = at<float>(bws, R.gk); a.gv = at<float>(bws, R.gv); a.gb_ = at<float>(bws, R.gb);
   a.coef = at<float>(bws, R.coef); a.da_part = at<float>(bws, R.da_part);
   a.da = a.centroids && a.mode ? at<float>(bws, R.da) : nullptr;
+  a.counter = at<int>(bws, R.counter);
   a.status = status;
   const cudaError_t e = launch_attn_bwd(a, p->D, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "sol_attn_bwd launch");

@@ -21,6 +21,7 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(256) stat_kernel(const BwdArgs a) {
   __shared__ float sd[kStatHeads][65];
   const int hg = (a.H + kStatHeads - 1) / kStatHeads, blk = blockIdx.x / hg % a.nb;
   const int b = blockIdx.x / hg / a.nb, h0 = (int)(blockIdx.x % hg) * kStatHeads;
+  if (blockIdx.x == 0 && threadIdx.x < 4) a.counter[threadIdx.x] = 0;   // the later passes' tile counters
   const int c = threadIdx.x % LPR, g = threadIdx.x / LPR;
 #pragma unroll 4
   for (int e = g; e < 64 * kStatHeads; e += G) {   // heads fastest: contiguous rows of BTHD
@@ -161,7 +163,11 @@ __global__ void __launch_bounds__(kTWarps * 32) tplan_kernel(const BwdArgs a) {
 // queue does not cover: while one warp waits the other's MMAs run.  Every wait is bounded; on expiry the kernel raises
 // SOL_ERR_TIMEOUT, drains what it issued and frees TMEM.
 constexpr int kThreads = 384;            // 4 control warps + 2 softmax warpgroups
-constexpr int kMaxWords = kMaxKeyBlocks / 32;
+constexpr unsigned kSms = 148;
+// A persistent CTA takes its next tile when this many steps of the present one are
+// left to load: early enough for its plan, late enough that a CTA in a long tile
+// does not hold a tile that another could run.
+constexpr int kAhead = 12;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -177,6 +183,27 @@ __device__ __forceinline__ void cta_sync() {
   __syncthreads();
 }
 
+// Bounded wait in as few instructions as it takes: false on expiry (recorded in the
+// abort flag, which the CTA reports at its end) or once another warp gave up.  These
+// kernels' code has to stay in the instruction cache: a first pass over straight
+// code costs some ten clocks an instruction (dq_kernel at N = 4096, H = 56: 184 us
+// with wait_bar's loop in every place and unrolled ways in and out, 146 without).
+__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t i = 0; !mbar_try(b, parity); ++i) {
+    if (*abort_flag) return false;
+    if (i >= kSpinLimit) { *abort_flag = 1; return false; }
+  }
+  return true;
+}
+// The same with its polling out of line.  Smaller still (dq_kernel above: 148 us
+// against 161), but a call costs registers: dkv_kernel's softmax threads spill.
+__device__ __noinline__ bool wait_poll(uint64_t* b, uint32_t parity, volatile int* abort_flag) {
+  return wait_for(b, parity, abort_flag);
+}
+__device__ __forceinline__ bool wait_call(uint64_t* b, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try(b, parity) || wait_poll(b, parity, abort_flag);
+}
+
 // Shared-memory and TMEM layout.  Streamed tiles are 64 rows in 128-byte column
 // chunks (SW128); the owned tiles of dkv_kernel are 128 rows.
 template <int D>
@@ -186,44 +213,67 @@ struct Cfg {
   static constexpr int kSTile = 64 * D * 2;           // streamed tile
   static constexpr int kOChunk = 128 * 128;           // one column chunk of an owned tile
   static constexpr int kOTile = 128 * D * 2;
-  static constexpr int kDqStages = 5, kKvStages = 4;  // pairs of streamed tiles in flight
+  static constexpr int kStages = 4;                    // dkv: pairs of streamed tiles in flight
+  static constexpr int kDqStages = 6;                  // dq: ring slots of one pair
   // TMEM columns.  dq: Q | dO | dQ | two stages; dkv: dV | dK | two stages.
   static constexpr uint32_t kStage = 256;             // stage g: S at kStage + 128 g, dP 64 columns on
   static constexpr uint32_t kQ = 0, kDo = 64, kDq = 128;
   static constexpr uint32_t kDv = 0, kDk = 128;
 };
 
-struct Bars {
-  uint64_t own_full;                // owned tiles have landed (dkv: TMA) / are in TMEM (dq: softmax threads)
-  uint64_t full[5], empty[5];       // ring of streamed tile pairs
-  uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
-  uint64_t p_full[2], ds_full[2];   // S is read (dq) or P is in its place (dkv) / dS is in dP's place
-  uint64_t own_tile;                // dq: Q and dO are in shared memory, on their way to TMEM
-  uint64_t cent_ready;              // dq: the centroids' offsets are in shared memory
-  uint64_t final_mma;
-};
-
-struct DqExtra {
-  Bars bar;
-  uint32_t tmem_base;
-  int abort_flag, n_union, n_cent;
-  uint32_t sel[2][kMaxWords];
+// What the roles of a persistent CTA read of a tile: its plan, in one of two
+// buffers filled by the planning warp while the previous tile runs.
+struct DqTile {
+  int tile, n_union, n_cent;                      // tile < 0: no more
   int list[kMaxKeyBlocks];                        // union entries: j | needA << 16 | needB << 17
   int clist[16];                                  // 64-centroid units: u | liveA << 16 | liveB << 17
   alignas(16) float cent_add[16][2][64];          // their offsets (log2 units), -inf where masked
+  __device__ __forceinline__ int steps() const { return n_union + n_cent; }
+  __device__ __forceinline__ int entry(int t) const { return *(t < n_union ? &list[t] : &clist[t - n_union]); }
+};
+struct DqBars {
+  uint64_t plan_full[2], plan_cent[2], plan_empty[2];   // a buffer's lists / centroid offsets are there; all roles are done
+  uint64_t plan_go;                 // time to take the next tile
+  uint64_t own_full[2], own_free[2];   // Q / dO are in TMEM; the tile's S / dP products have read them
+  uint64_t full[6], empty[6];       // ring slots
+  uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
+  uint64_t p_full[2], ds_full[2];   // S is read / dS is in dP's place
+  uint64_t dq_full, dq_clear;       // the tile's dQ is complete / read and zeroed for the next tile
+  uint64_t out_full;                // dQ is in its ring slot, to be stored
+  uint64_t mma_done;                // the issuers' last commits, at the end
+};
+struct DqExtra {
+  DqBars bar;
+  uint32_t tmem_base;
+  int abort_flag;
   alignas(16) float tail_add[64];                 // 0 for valid rows of the last key block, -inf past N
+  DqTile info[2];
 };
 
-template <int S>
-struct KvExtra {
-  Bars bar;
-  uint32_t tmem_base;
-  int abort_flag, n_steps;
+struct KvTile {
+  int tile, n;                                    // tile < 0: no more
   int list[kMaxKeyBlocks];                        // query blocks: i | needA << 16 | needB << 17
-  uint32_t cword[128][4];                         // centroids: the step's exact-block bits of this tile
-  alignas(16) float nl[S][64], nd[S][64];         // per ring stage: -lse, -delta of the query rows
+  uint32_t cword[128][4];                         // centroids: each step's exact-block bits of the tile
   alignas(16) float gsum[2][2][128];              // exact: the two blocks' gk, gv
-  float gb[128];
+};
+struct KvBars {
+  uint64_t plan_full[2], plan_cent[2], plan_empty[2];   // a buffer's list / centroid sums are there; all roles are done
+  uint64_t plan_go;                 // time to take the next tile
+  uint64_t own_full[2], own_free[2];   // the tile's K / V are in shared memory; its S / dP products have read them
+  uint64_t full[4], empty[4];       // ring slots
+  uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
+  uint64_t p_full[2], ds_full[2];   // P is in S's place / dS is in dP's place
+  uint64_t acc_full[2], acc_clear[2];   // dK / dV are complete; read and zeroed for the next tile
+  uint64_t gb_full, out_full;       // group 0's offset sums are there; the results are in their ring slots, to be stored
+  uint64_t mma_done;                // the issuers' last commits, at the end
+};
+struct KvExtra {
+  KvBars bar;
+  uint32_t tmem_base;
+  int abort_flag;
+  alignas(16) float nl[4][64], nd[4][64];         // per ring slot: -lse, -delta of the query rows
+  float gb[2][128];
+  KvTile info[2];
 };
 
 // TMA loads of one streamed pair (two 64-row tiles).
@@ -239,6 +289,15 @@ __device__ __forceinline__ void load_pair4(uint8_t* dst, const CUtensorMap* m1, 
 // Rows of half hf that a step with this list entry leaves out of its MMAs.
 __device__ __forceinline__ uint32_t off(int entry, int hf) { return (entry >> (16 + hf)) & 1 ? 0u : 0xffffffffu; }
 
+// The i-th of all heads' tiles (`per` a head) in the order in which they are run:
+// every head's first `lead` tiles, the prefix's, whose lists are the longest, then
+// the others, head by head (neighbours share K and V, or Q and dO, in L2).
+__device__ __forceinline__ int tile_at(int i, int heads, int per, int lead) {
+  if (i < heads * lead) return i / lead * per + i % lead;
+  i -= heads * lead;
+  return i / (per - lead) * per + lead + i % (per - lead);
+}
+
 // Position in the ring of streamed tiles: stage and the parity of its current load.
 template <int S>
 struct RingPos {
@@ -246,6 +305,11 @@ struct RingPos {
   uint32_t ph = 0;
   __device__ __forceinline__ void next() {
     if (++s == S) { s = 0; ph ^= 1u; }
+  }
+  __device__ __forceinline__ void skip(int n) {
+    s += n;
+    ph ^= (uint32_t)(s / S) & 1u;
+    s %= S;
   }
 };
 
@@ -256,14 +320,14 @@ __device__ __forceinline__ uint64_t kmaj(uint64_t base, int kk, int chunk) {
   return base + (uint64_t)(((kk >> 2) * chunk + (kk & 3) * 32) >> 4);
 }
 
-// Row r's 32 values of columns 32c .. 32c+31, as bf16, into a SW128 tile of 128 rows
+// Row r's 16 values of columns 16c .. 16c+15, as bf16, into a SW128 tile of 128 rows
 // (64-column chunks), the layout of the tile stores.
 template <int D>
 __device__ __forceinline__ void put_row(uint8_t* tile, int r, int c, const float* v) {
-  uint8_t* row = tile + (c >> 1) * Cfg<D>::kOChunk + r * 128;
+  uint8_t* row = tile + (c >> 2) * Cfg<D>::kOChunk + r * 128;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int at = 4 * (c & 1) + u;
+  for (int u = 0; u < 2; ++u) {
+    const int at = 2 * (c & 3) + u;
     *reinterpret_cast<uint4*>(row + ((at ^ (r & 7)) << 4)) =
         make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
                    pack_bf16(v[8 * u + 4], v[8 * u + 5]), pack_bf16(v[8 * u + 6], v[8 * u + 7]));
@@ -279,432 +343,541 @@ __device__ __forceinline__ void store_rows(const CUtensorMap* m, const uint8_t* 
   tma_store_wait();
 }
 
+// The queries' pass is persistent: a CTA takes tiles off a counter until none is
+// left.  While a tile runs, its planning warp fetches the next one's lists; the
+// loading warp runs ahead through one ring of 32 KB slots, which carry for each
+// tile Q, dO, the steps' K and V and, last, dQ on its way out.  The next tile's
+// Q and dO go into TMEM as soon as this one's products have read theirs, so its
+// first S and dP are computed while dQ is brought out; only dQ's accumulator is
+// waited for.  Steps, slots and barrier phases count on through the tiles.  (A CTA
+// per tile spent 12,000 clocks around its steps: launch, plan, loads, the first
+// products and the way out.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo, const __grid_constant__ CUtensorMap mdq,
           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
           const __grid_constant__ CUtensorMap mkb, const __grid_constant__ CUtensorMap mvb, const BwdArgs a) {
   using C = Cfg<D>;
+  constexpr int S = C::kDqStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* own = ring + (C::kDqStages - 2) * 2 * C::kSTile;   // Q, dO at the start; the ring's last two stages after
-  DqExtra& x = *reinterpret_cast<DqExtra*>(ring + C::kDqStages * 2 * C::kSTile);
-  Bars& bar = x.bar;
+  static_assert(C::kOTile == 2 * C::kSTile, "a slot holds a streamed pair or one owned tile");
+  DqExtra& x = *reinterpret_cast<DqExtra*>(ring + S * 2 * C::kSTile);
+  DqBars& bar = x.bar;
   volatile int* abort_flag = &x.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntq = (a.nb + 1) / 2, mw = a.mask_words;
-  const int tq = blockIdx.x % ntq;
-  const int64_t bh = blockIdx.x / ntq;
-  const int b = (int)(bh / a.H), h = (int)(bh % a.H), i0 = 2 * tq;
 
   if (tid == 0) {
-    mbar_init(&bar.own_full, 256);
-    mbar_init(&bar.own_tile, 1);
-    mbar_init(&bar.cent_ready, 1);
-    for (int s = 0; s < C::kDqStages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.plan_full[s], 1); mbar_init(&bar.plan_cent[s], 1); mbar_init(&bar.plan_empty[s], 1 + 2 + 8);
       mbar_init(&bar.s_full[s], 1); mbar_init(&bar.dp_full[s], 1);
       mbar_init(&bar.p_full[s], 4); mbar_init(&bar.ds_full[s], 4);
     }
-    mbar_init(&bar.final_mma, 2);
+    for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&bar.own_full[s], 128); mbar_init(&bar.own_free[s], 1); }
+    mbar_init(&bar.dq_full, 1);
+    mbar_init(&bar.dq_clear, 256);
+    mbar_init(&bar.out_full, 8);
+    mbar_init(&bar.plan_go, 1);
+    mbar_init(&bar.mma_done, 2);
     x.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    // Q and dO rest in the ring's last two stages until the softmax threads have them
-    // in TMEM (row-per-thread global loads instead held up the plan's by 3,000 clocks)
-    mbar_expect_tx(&bar.own_tile, 2 * C::kOTile);
-    for (int c = 0; c < C::kChunks; ++c)
-      for (int hf = 0; hf < 2; ++hf) {
-        tma_load_4d(own + c * C::kOChunk + hf * (C::kOChunk / 2), &mq, c * 64, h, 64 * (i0 + hf), b, &bar.own_tile);
-        tma_load_4d(own + C::kOTile + c * C::kOChunk + hf * (C::kOChunk / 2), &mdo, c * 64, h, 64 * (i0 + hf), b, &bar.own_tile);
-      }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&x.tmem_base)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  const int n_tail = a.N - 64 * (a.nb - 1);
-  if (tid < 64) x.tail_add[tid] = tid < n_tail ? 0.f : -INFINITY;
-  {
-    const int* P = a.plan + (bh * ntq + tq) * plan_ints(mw, a.nb);
-    for (int e = tid; e < 2 * mw + a.nb; e += kThreads) {
-      const int v = P[16 + e];
-      if (e >= 2 * mw) x.list[e - 2 * mw] = v;
-      else x.sel[e / mw][e % mw] = (uint32_t)v;
-    }
-    if (tid < 32) {   // 64-centroid units (two bitmap words) that either query block leaves to its centroids
-      const uint32_t w0 = (uint32_t)P[12], w1 = (uint32_t)P[13];
-      const bool l0 = tid < 16 && ((w0 >> (2 * tid)) & 3u), l1 = tid < 16 && ((w1 >> (2 * tid)) & 3u);
-      const uint32_t any = __ballot_sync(0xffffffffu, l0 || l1);
-      if (l0 || l1) x.clist[__popc(any & ((1u << tid) - 1u))] = tid | (int)l0 << 16 | (int)l1 << 17;
-      if (tid == 0) { x.n_union = P[0]; x.n_cent = __popc(any); }
-    }
-  }
+  if (tid < 64) x.tail_add[tid] = tid < a.N - 64 * (a.nb - 1) ? 0.f : -INFINITY;
   fence_before();
   cta_sync();
   fence_after();
   const uint32_t tmem = x.tmem_base;
-  const int n_union = x.n_union, T = n_union + x.n_cent;
-  auto entry = [&](int t) { return *(t < n_union ? &x.list[t] : &x.clist[t - n_union]); };
+  // every wait's outcome is made warp-uniform where a whole warp takes part
+  auto wait = [&](uint64_t* b, uint32_t par) { return wait_call(b, par & 1u, abort_flag); };
+  auto wait_w = [&](uint64_t* b, uint32_t par) { return __all_sync(0xffffffffu, wait(b, par)) != 0; };
+
   if (warp == 0) {
-    if (lane == 0) {   // K and V (centroid) tiles
-      int nl = 0;
-      for (int t = 0; t < T; ++t) {
-        const int s = t % C::kDqStages, n = t / C::kDqStages;
-        if (!wait_bar(&bar.empty[s], (n & 1) ^ 1, abort_flag, a.status)) break;
-        if (t == C::kDqStages - 2 && !wait_bar(&bar.own_full, 0, abort_flag, a.status)) break;
-        uint8_t* dst = ring + s * 2 * C::kSTile;
-        ++nl;
-        mbar_expect_tx(&bar.full[s], 2 * C::kSTile);
-        if (t < n_union) {
-          load_pair4<D>(dst, &mk, &mv, 64 * (x.list[t] & 0xffff), h, b, &bar.full[s]);
-        } else {
-          const int row = 64 * (x.clist[t - n_union] & 0xffff);
-          for (int c = 0; c < C::kChunks; ++c) {
-            tma_load_3d(dst + c * C::kSChunk, &mkb, c * 64, row, (int)bh, &bar.full[s]);
-            tma_load_3d(dst + C::kSTile + c * C::kSChunk, &mvb, c * 64, row, (int)bh, &bar.full[s]);
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      RingPos<S> pos;
+      int slots = 0;
+      bool ok = true;
+      auto slot = [&]() { return ok = ok && wait(&bar.empty[pos.s], pos.ph ^ 1u); };
+      auto next = [&]() { pos.next(); ++slots; };
+      for (int k = 0;; ++k) {
+        if (!(ok = ok && wait(&bar.plan_full[k & 1], k >> 1))) break;
+        const DqTile& in = x.info[k & 1];
+        if (in.tile < 0) break;
+        const int64_t bh = in.tile / ntq;
+        const int i0 = 2 * (in.tile % ntq), h = (int)(bh % a.H), b = (int)(bh / a.H), T = in.steps();
+        for (int o = 0; o < 2 && slot(); ++o, next()) {   // Q, dO
+          mbar_expect_tx(&bar.full[pos.s], C::kOTile);
+          for (int c = 0; c < C::kChunks; ++c)
+            for (int hf = 0; hf < 2; ++hf)
+              tma_load_4d(ring + pos.s * C::kOTile + c * C::kOChunk + hf * (C::kOChunk / 2), o ? &mdo : &mq, c * 64, h, 64 * (i0 + hf), b,
+                          &bar.full[pos.s]);
+        }
+        const int go = max(0, T - kAhead);
+        if (T == 0) mbar_arrive(&bar.plan_go);
+        for (int t = 0; t < T && slot(); ++t, next()) {
+          if (t == go) mbar_arrive(&bar.plan_go);
+          uint8_t* dst = ring + pos.s * C::kOTile;
+          uint64_t* full = &bar.full[pos.s];
+          mbar_expect_tx(full, 2 * C::kSTile);
+          const int row = 64 * (in.entry(t) & 0xffff);
+          if (t < in.n_union) {
+            load_pair4<D>(dst, &mk, &mv, row, h, b, full);
+          } else {
+            for (int c = 0; c < C::kChunks; ++c) {
+              tma_load_3d(dst + c * C::kSChunk, &mkb, c * 64, row, (int)bh, full);
+              tma_load_3d(dst + C::kSTile + c * C::kSChunk, &mvb, c * 64, row, (int)bh, full);
+            }
           }
         }
+        if (!slot()) break;   // the slot that carries dQ out: handed over empty
+        mbar_arrive(&bar.full[pos.s]);
+        next();
+        mbar_arrive(&bar.plan_empty[k & 1]);
       }
-      for (int s = 0; s < C::kDqStages; ++s) {   // every armed load has landed before the CTA may exit
-        const int cnt = (nl + C::kDqStages - 1 - s) / C::kDqStages;
-        if (cnt) drain_bar(&bar.full[s], (cnt - 1) & 1, a.status);
-      }
-      drain_bar(&bar.own_tile, 0, a.status);
+      // every armed load has landed before the CTA may exit
+      for (int i = max(0, slots - S); i < slots; ++i) drain_bar(&bar.full[i % S], (i / S) & 1, a.status);
     }
   } else if (warp == 1 || warp == 2) {
+    // ---------------------------------------------------------------- products
     constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
     constexpr uint64_t kStep = 2 * (C::kSTile >> 4);   // descriptor step per ring stage
     const uint64_t sd0 = sdesc(smem_u32(ring), 16, 1024), gd0 = sdesc(smem_u32(ring), C::kSChunk, 1024);
-    RingPos<C::kDqStages> ld, use;   // the next step to start, the step to finish
-    auto wait_ld = [&]() { return wait_bar(&bar.full[ld.s], ld.ph, abort_flag, a.status); };
+    RingPos<S> ld, use;   // the next step to start, the step to finish
+    auto wait_ld = [&]() { return wait(&bar.full[ld.s], ld.ph); };
     // A(TMEM) times a streamed tile: S from Q and K, dP from dO and V.  Half-way
     // through, the next step's barriers are looked at: the answer comes back while
     // the second half is issued, and a step whose barriers are already complete
     // (the usual case) starts without a wait.
-    auto start = [&](uint32_t col, uint32_t own, uint64_t bd, uint64_t* done, int e, auto&& probe) {
+    auto start = [&](uint32_t col, uint32_t own_col, uint64_t bd, uint64_t* done, int e, auto&& probe) {
       const uint64_t b0 = bd + ld.s * kStep;
       ld.next();
       bool r = false;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         if (kk == D / 32) r = probe();
-        mma_ts_m(tmem + col, tmem + own + kk * 8, kmaj<D>(b0, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u, off(e, 0), off(e, 1));
+        mma_ts_m(tmem + col, tmem + own_col + kk * 8, kmaj<D>(b0, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u, off(e, 0), off(e, 1));
       }
       mma_commit_w(done);
       return r;
     };
-    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
-    fence_after();
-    if (warp == 1) {   // S(t+2) once S(t) is in the softmax threads' registers
-      bool early = false;
-      int e0 = T > 0 ? entry(0) : 0;
-      for (int t = 0; t < T && ok; ++t) {
-        const uint32_t par = ((t >> 1) & 1) ^ 1;
-        if (!__all_sync(0xffffffffu, early)) {
-          ok = wait_ld() && (t < 2 || wait_bar(&bar.p_full[t & 1], par, abort_flag, a.status));
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+    bool ok = true;
+    int base = 0;   // steps of the earlier tiles
+    for (int k = 0; ok; ++k) {
+      if (!(ok = wait_w(&bar.plan_full[k & 1], k >> 1))) break;
+      const DqTile& in = x.info[k & 1];
+      if (in.tile < 0) break;
+      const int T = in.steps(), o = warp - 1;
+      if (!(ok = wait_w(&bar.own_full[o], k))) break;
+      fence_after();
+      if (o) ld.next();
+      if (lane == 0) mbar_arrive(&bar.empty[ld.s]);   // Q's / dO's slot
+      ld.skip(2 - o);
+      if (warp == 1) {   // S(u+2) once S(u) is in the softmax threads' registers (u counts through the tiles)
+        bool early = false;
+        int e0 = T > 0 ? in.entry(0) : 0;
+        for (int u = base; u < base + T && ok; ++u) {
+          const uint32_t par = ((u >> 1) & 1) ^ 1;
+          if (!__all_sync(0xffffffffu, early)) {
+            ok = wait_ld() && (u < 2 || wait(&bar.p_full[u & 1], par));
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          }
+          fence_after();
+          const int e = e0;
+          early = start(C::kStage + 128 * (u & 1), C::kQ, sd0, &bar.s_full[u & 1], e, [&]() {
+            const bool l = mbar_test(&bar.full[ld.s], ld.ph);
+            e0 = in.entry(min(u + 1 - base, T - 1));
+            return (u + 1 < 2 || mbar_test(&bar.p_full[(u + 1) & 1], (((u + 1) >> 1) & 1) ^ 1)) && l;
+          });
         }
+        mma_commit_w(&bar.own_free[0]);
+      } else {           // dQ += dS(u) K, then dP(u+2) over dS(u)
+        for (int t = 0; t < 2 && t < T && ok; ++t)
+          if ((ok = __all_sync(0xffffffffu, wait_ld())))
+            start(C::kStage + 128 * ((base + t) & 1) + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[(base + t) & 1], in.entry(t),
+                  []() { return false; });
+        use.skip(2);
+        if (!(ok = ok && wait_w(&bar.dq_clear, k))) break;
         fence_after();
-        const int e = e0;
-        early = start(C::kStage + 128 * (t & 1), C::kQ, sd0, &bar.s_full[t & 1], e, [&]() {
-          const int u = t + 1;
-          const bool l = mbar_test(&bar.full[ld.s], ld.ph);
-          e0 = entry(min(u, T - 1));
-          return (u < 2 || mbar_test(&bar.p_full[u & 1], ((u >> 1) & 1) ^ 1)) && l;
-        });
-      }
-    } else {           // dQ += dS(t) K, then dP(t+2) over dS(t)
-      for (int t = 0; t < 2 && t < T && ok; ++t)
-        if ((ok = __all_sync(0xffffffffu, wait_ld())))
-          start(C::kStage + 128 * t + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t], entry(t), []() { return false; });
-      auto dq_mma = [&](int t, int e) {
+        auto dq_mma = [&](int u, int e) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ts_m(tmem + C::kDq, tmem + C::kStage + 128 * (t & 1) + 64 + kk * 8, gd0 + use.s * kStep + (uint64_t)(kk * 2048 >> 4),
-                   id_g, 1u, off(e, 0), off(e, 1));
-        mma_commit_w(&bar.empty[use.s]);   // S(t), on which dS(t) depends, has read its tile too
-        use.next();
-      };
-      bool early = false;
-      int t = 0, e0 = T > 0 ? entry(0) : 0, e1 = T > 1 ? entry(1) : 0, e2 = T > 2 ? entry(2) : 0;   // steps t, t+1, t+2
-      for (; t < T - 2 && ok; ++t) {   // (no condition around a batch: see the last two steps below)
-        if (!__all_sync(0xffffffffu, early)) {
-          ok = wait_ld() && wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts_m(tmem + C::kDq, tmem + C::kStage + 128 * (u & 1) + 64 + kk * 8, gd0 + use.s * kStep + (uint64_t)(kk * 2048 >> 4),
+                     id_g, 1u, off(e, 0), off(e, 1));
+          mma_commit_w(&bar.empty[use.s]);   // S(u), on which dS(u) depends, has read its tile too
+          use.next();
+        };
+        bool early = false;
+        int u = base, e0 = T > 0 ? in.entry(0) : 0, e1 = T > 1 ? in.entry(1) : 0, e2 = T > 2 ? in.entry(2) : 0;   // steps u, u+1, u+2
+        for (; u < base + T - 2 && ok; ++u) {   // (no condition around a batch: see the last two steps below)
+          if (!__all_sync(0xffffffffu, early)) {
+            ok = wait_ld() && wait(&bar.ds_full[u & 1], u >> 1);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          }
+          fence_after();
+          dq_mma(u, e0);
+          const int e = e2;
+          e0 = e1;
+          e1 = e2;
+          early = start(C::kStage + 128 * (u & 1) + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[u & 1], e, [&]() {
+            const bool l = mbar_test(&bar.full[ld.s], ld.ph);
+            e2 = in.entry(min(u + 3 - base, T - 1));
+            return mbar_test(&bar.ds_full[(u + 1) & 1], ((u + 1) >> 1) & 1) && l;
+          });
         }
-        fence_after();
-        dq_mma(t, e0);
-        const int e = e2;
-        e0 = e1;
-        e1 = e2;
-        early = start(C::kStage + 128 * (t & 1) + 64, C::kDo, sd0 + (C::kSTile >> 4), &bar.dp_full[t & 1], e, [&]() {
-          const bool l = mbar_test(&bar.full[ld.s], ld.ph);
-          e2 = entry(min(t + 3, T - 1));
-          return mbar_test(&bar.ds_full[(t + 1) & 1], ((t + 1) >> 1) & 1) && l;
-        });
+        mma_commit_w(&bar.own_free[1]);
+        for (; u < base + T && ok; ++u) {
+          if (!(ok = wait_w(&bar.ds_full[u & 1], u >> 1))) break;
+          fence_after();
+          dq_mma(u, e0);
+          e0 = e1;
+        }
+        mma_commit_w(&bar.dq_full);
+        use.next();   // dQ's slot
       }
-      for (; t < T && ok; ++t) {
-        if (!(ok = __all_sync(0xffffffffu, wait_bar(&bar.ds_full[t & 1], (t >> 1) & 1, abort_flag, a.status)))) break;
-        fence_after();
-        dq_mma(t, e0);
-        e0 = e1;
+      ld.next();      // dQ's slot
+      base += T;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.plan_empty[k & 1]);
+    }
+    mma_commit_w(&bar.mma_done);
+    if (warp == 1) drain_bar(&bar.mma_done, 0, a.status);
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- plans, and dQ's way out
+    const int total = a.B * a.H * ntq;
+    auto plan = [&](int k) {   // the next tile off the counter into buffer k & 1
+      DqTile& in = x.info[k & 1];
+      int tile = 0;
+      if (lane == 0) tile = atomicAdd(a.counter, 1);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
+      if (tile >= total) {
+        if (lane == 0) { in.tile = -1; mbar_arrive(&bar.plan_full[k & 1]); }
+        return;
       }
+      tile = tile_at(tile, a.B * a.H, ntq, min(ntq, (a.prefix + 127) / 128));
+      const int* P = a.plan + (int64_t)tile * plan_ints(mw, a.nb);
+      const int n = P[0];
+      const uint32_t w0 = (uint32_t)P[12], w1 = (uint32_t)P[13];   // bitmap words that leave a block to its centroid
+      const bool l0 = lane < 16 && ((w0 >> (2 * lane)) & 3u), l1 = lane < 16 && ((w1 >> (2 * lane)) & 3u);
+      const uint32_t any = __ballot_sync(0xffffffffu, l0 || l1);
+      if (l0 || l1) in.clist[__popc(any & ((1u << lane) - 1u))] = lane | (int)l0 << 16 | (int)l1 << 17;
+#pragma unroll 4
+      for (int e = lane; e < n; e += 32) in.list[e] = P[16 + 2 * mw + e];
+      if (lane == 0) { in.tile = tile; in.n_union = n; in.n_cent = __popc(any); }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.plan_full[k & 1]);
+      const int64_t bh = tile / ntq;
+      const int i0 = 2 * (tile % ntq), nc = __popc(any);
+      for (int s = 0; s < nc; ++s) {
+        const int unit = in.clist[s] & 0xffff;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = lane + 32 * q, hf = e >> 6, j = 64 * unit + (e & 63);
+          float v = -INFINITY;
+          if (j < a.nb && i0 + hf < a.nb && !(((uint32_t)P[16 + hf * mw + (j >> 5)] >> (j & 31)) & 1u)) v = a.cbias[bh * a.nb + j] * kLog2e;
+          in.cent_add[s][hf][e & 63] = v;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.plan_cent[k & 1]);
+    };
+    RingPos<S> pos;
+    plan(0);
+    for (int k = 0;; ++k) {
+      const DqTile& in = x.info[k & 1];
+      if (in.tile < 0) break;
+      if (!wait_w(&bar.plan_go, k) || (k >= 1 && !wait_w(&bar.plan_empty[(k + 1) & 1], ((k + 1) >> 1) - 1))) break;
+      plan(k + 1);
+      pos.skip(2 + in.steps());
+      if (!wait_w(&bar.out_full, k)) break;
+      if (lane == 0) {
+        store_rows<D>(&mdq, ring + pos.s * C::kOTile, 128 * (in.tile % ntq), (in.tile / ntq) % a.H, in.tile / ntq / a.H, a.N);
+        mbar_arrive(&bar.empty[pos.s]);
+      }
+      pos.next();
+      __syncwarp();
     }
-    mma_commit_w(&bar.final_mma);
-    if (warp == 1) drain_bar(&bar.final_mma, 0, a.status);
-  } else if (warp == 3) {   // the centroids' offsets, needed after the last listed block
-    for (int e = lane; e < 128 * x.n_cent; e += 32) {
-      const int slot = e >> 7, hf = (e >> 6) & 1, j = 64 * (x.clist[slot] & 0xffff) + (e & 63);
-      const bool live = j < a.nb && i0 + hf < a.nb && !((x.sel[hf][j >> 5] >> (j & 31)) & 1u);
-      x.cent_add[slot][hf][e & 63] = live ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar.cent_ready);
-  } else if (warp >= 4) {
+  } else {
+    // ---------------------------------------------------------------- softmax warpgroups
     const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
-    const int row = 64 * i0 + r;
-    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_tile, 0, abort_flag, a.status));
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
-    {   // group 0 puts Q, group 1 dO into TMEM
-#pragma unroll
+    const float sl2 = a.scale * kLog2e;
+    const uint64_t sl22 = f2pack(sl2, sl2);
+    int base = 0;        // steps of the earlier tiles
+    RingPos<S> pos;      // the tile's first slot
+    float nl = 0.f, nd = 0.f;
+    // A tile's rows: -lse and -delta, and Q (group 0) or dO (group 1) from its slot into TMEM
+    auto take_own = [&](const DqTile& in) {
+      const int i = 2 * (in.tile % ntq) + hf;
+      const int64_t at = (int64_t)(in.tile / ntq) * 64 * a.nb + 64 * i + (r & 63);
+      nl = i < a.nb ? a.nlse[at] : -INFINITY;
+      nd = i < a.nb ? a.ndelta[at] : 0.f;
+      RingPos<S> p = pos;
+      if (g) p.next();
+      if (!wait_w(&bar.full[p.s], p.ph)) return false;
+      const uint8_t* src = ring + p.s * C::kOTile + r * 128;
+#pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t w[32];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const uint4 v = *reinterpret_cast<const uint4*>(own + g * C::kOTile + c * C::kOChunk + r * 128 + ((u ^ (r & 7)) << 4));
+          const uint4 v = *reinterpret_cast<const uint4*>(src + c * C::kOChunk + ((u ^ (r & 7)) << 4));
           w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
         }
         tmem_st32(lane_addr + (g == 0 ? C::kQ : C::kDo) + 32 * c, w);
-#pragma unroll
-        for (int u = 0; u < 32; ++u) w[u] = 0u;
-        tmem_st32(lane_addr + C::kDq + g * (D / 2) + 32 * c, w);   // dQ starts from zero (its half)
       }
       tmem_wait_st();
-      fence_async();   // the rows are read before the ring's loads overwrite them
+      fence_async();   // the rows are read before later loads overwrite the slot
       fence_before();
-      mbar_arrive(&bar.own_full);
+      mbar_arrive(&bar.own_full[g]);
+      return true;
+    };
+    // dQ starts from zero: each group clears the columns that it brings out (16 at a time)
+    auto clear = [&](int c) {
+      uint32_t z[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) z[u] = 0u;
+      tmem_st16(lane_addr + C::kDq + 16 * c, z);
+    };
+    bool ok = wait_w(&bar.plan_full[0], 0);
+    if (ok && x.info[0].tile >= 0) {
+      ok = take_own(x.info[0]);
+#pragma unroll 1
+      for (int c = g; c < D / 16; c += 2) clear(c);
+      tmem_wait_st();
+      fence_before();
+      mbar_arrive(&bar.dq_clear);
     }
-    const bool in_range = i0 + hf < a.nb;
-    const float nl = in_range ? a.nlse[bh * 64 * a.nb + row] : -INFINITY;
-    const float nd = in_range ? a.ndelta[bh * 64 * a.nb + row] : 0.f;
-    const float sl2 = a.scale * kLog2e;
-    const uint64_t sl22 = f2pack(sl2, sl2), nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
-    for (int t = g; t < T && ok; t += 2) {
-      const float* add = nullptr;
-      const int e = entry(t);
-      const bool need = (e >> (16 + hf)) & 1;
-      if (t < n_union) {
-        if ((e & 0xffff) == a.nb - 1) add = x.tail_add;
-      } else {
-        if (t < n_union + 2) ok = __all_sync(0xffffffffu, wait_bar(&bar.cent_ready, 0, abort_flag, a.status));
-        if (!ok) break;
-        add = x.cent_add[t - n_union][hf];
-      }
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.s_full[g], (t >> 1) & 1, abort_flag, a.status));
-      if (!ok) break;
-      fence_after();
-      const uint32_t st = lane_addr + C::kStage + 128 * g;
-      float p[64];
-      if (need) {
-        tmem_ld32(st, p);
-        tmem_ld32(st + 32, p + 32);
-        tmem_wait_ld();
-      }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[g]);
-      if (need) {
-        uint64_t mul2 = sl22;
-        if (add) {   // centroids and the last key block: offsets first (log2 units)
+    for (int k = 0; ok; ++k) {
+      const DqTile& in = x.info[k & 1];
+      if (in.tile < 0) break;
+      const int n_union = in.n_union, T = in.steps(), tile = in.tile;
+      const uint64_t nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
+      for (int u = base + ((base + g) & 1); u < base + T; u += 2) {   // the steps of this group's stage
+        const int t = u - base, e = in.entry(t);
+        const bool need = (e >> (16 + hf)) & 1;
+        const float* add = nullptr;
+        if (t < n_union) {
+          if ((e & 0xffff) == a.nb - 1) add = x.tail_add;
+        } else {
+          if (!(ok = wait_w(&bar.plan_cent[k & 1], k >> 1))) break;
+          add = in.cent_add[t - n_union][hf];
+        }
+        if (!(ok = wait_w(&bar.s_full[g], u >> 1))) break;
+        fence_after();
+        const uint32_t st = lane_addr + C::kStage + 128 * g;
+        float p[64];
+        if (need) {
+          tmem_ld32(st, p);
+          tmem_ld32(st + 32, p + 32);
+          tmem_wait_ld();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[g]);
+        if (need) {
+          uint64_t mul2 = sl22;
+          if (add) {   // centroids and the last key block: offsets first (log2 units)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float2 o = reinterpret_cast<const float2*>(add)[c];
+              f2unpack(ffma2(f2pack(p[2 * c], p[2 * c + 1]), sl22, f2pack(o.x, o.y)), p[2 * c], p[2 * c + 1]);
+            }
+            mul2 = f2pack(1.f, 1.f);
+          }
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const float2 o = reinterpret_cast<const float2*>(add)[c];
-            f2unpack(ffma2(f2pack(p[2 * c], p[2 * c + 1]), sl22, f2pack(o.x, o.y)), p[2 * c], p[2 * c + 1]);
-          }
-          mul2 = f2pack(1.f, 1.f);
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float e0, e1;
-          f2unpack(ffma2(f2pack(p[2 * c], p[2 * c + 1]), mul2, nl2), e0, e1);
-          p[2 * c] = ex2(e0);
-          p[2 * c + 1] = ex2(e1);
-        }
-      }
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.dp_full[g], (t >> 1) & 1, abort_flag, a.status));
-      if (!ok) break;
-      fence_after();
-      if (need) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float dp[32];
-          tmem_ld32(st + 64 + 32 * hh, dp);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int k = 32 * hh + 2 * c;
-            float d0, d1;
-            f2unpack(fmul2(f2pack(p[k], p[k + 1]), fadd2(f2pack(dp[2 * c], dp[2 * c + 1]), nd2)), d0, d1);
-            pk[16 * hh + c] = pack_bf16(d0, d1);
+            float e0, e1;
+            f2unpack(ffma2(f2pack(p[2 * c], p[2 * c + 1]), mul2, nl2), e0, e1);
+            p[2 * c] = ex2(e0);
+            p[2 * c + 1] = ex2(e1);
           }
         }
-        tmem_st32(st + 64, pk);
-        tmem_wait_st();
-      }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.ds_full[g]);
-    }
-    if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
-    __syncwarp();
-    if (ok) {
-      fence_after();
-      const bool anch = a.da && (row >= a.prefix || a.prefix == a.N);
-      const float4* da = reinterpret_cast<const float4*>(a.da + bh * D);
-      for (int c = g; c < D / 32; c += 2) {
-        float v[32];
+        if (!(ok = wait_w(&bar.dp_full[g], u >> 1))) break;
+        fence_after();
+        if (need) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float dp[32];
+            tmem_ld32(st + 64 + 32 * hh, dp);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const int q = 32 * hh + 2 * c;
+              float d0, d1;
+              f2unpack(fmul2(f2pack(p[q], p[q + 1]), fadd2(f2pack(dp[2 * c], dp[2 * c + 1]), nd2)), d0, d1);
+              pk[16 * hh + c] = pack_bf16(d0, d1);
+            }
+          }
+          tmem_st32(st + 64, pk);
+          tmem_wait_st();
+        }
+        fence_before();
         __syncwarp();
-        tmem_ld32(lane_addr + C::kDq + 32 * c, v);
+        if (lane == 0) mbar_arrive(&bar.ds_full[g]);
+      }
+      if (!ok) break;
+      base += T;
+      RingPos<S> out = pos;
+      out.skip(2 + T);
+      pos = out;
+      pos.next();
+      // the next tile's rows, once this tile's products have read its own
+      if (!(ok = wait_w(&bar.plan_full[(k + 1) & 1], (k + 1) >> 1))) break;
+      const bool more = x.info[(k + 1) & 1].tile >= 0;
+      if (more && !(ok = wait_w(&bar.own_free[g], k) && take_own(x.info[(k + 1) & 1]))) break;
+      // dQ into its slot, from where the planning warp stores it
+      if (!(ok = wait_w(&bar.dq_full, k) && wait_w(&bar.full[out.s], out.ph))) break;
+      fence_after();
+      const int row = 128 * (tile % ntq) + r;
+      const bool anch = a.da && (row >= a.prefix || a.prefix == a.N);
+      const float4* da = reinterpret_cast<const float4*>(a.da + (int64_t)(tile / ntq) * D);
+#pragma unroll 1
+      for (int c = g; c < D / 16; c += 2) {
+        float v[16];
+        tmem_ld16(lane_addr + C::kDq + 16 * c, v);
         tmem_wait_ld();
+        clear(c);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] *= a.scale;
+        for (int e = 0; e < 16; ++e) v[e] *= a.scale;
         if (anch) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 d = da[8 * c + e];
+          for (int e = 0; e < 4; ++e) {
+            const float4 d = da[4 * c + e];
             v[4 * e] += d.x; v[4 * e + 1] += d.y; v[4 * e + 2] += d.z; v[4 * e + 3] += d.w;
           }
         }
-        put_row<D>(ring, r, c, v);   // the ring is idle: every step is complete
+        put_row<D>(ring + out.s * C::kOTile, r, c, v);
+        __syncwarp();
       }
+      tmem_wait_st();
       fence_async();
+      fence_before();
+      mbar_arrive(&bar.dq_clear);
+      __syncwarp();
+      if (lane == 0) { mbar_arrive(&bar.out_full); mbar_arrive(&bar.plan_empty[k & 1]); }
     }
-    bar_sync(1, 256);
-    if (tid == 128 && ok && !*abort_flag) store_rows<D>(&mdq, ring, 64 * i0, h, b, a.N);
   }
   fence_before();
   cta_sync();
+  if (tid == 0 && x.abort_flag) raise_status(a.status, SOL_ERR_TIMEOUT);
   if (warp == 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
   }
 }
 
+// The keys' pass (and, kCent, the centroids'), persistent like the queries': a tile
+// is 128 key rows (128 centroids and one range of the query blocks), its K and V
+// stay in shared memory, and the ring's slots carry the steps' Q and dO and then
+// dK and dV (fp32 gk and gv) on their way out.  The next tile's K and V are loaded
+// as soon as this tile's products have read theirs.
 template <int D, bool kCent>
 __global__ void __launch_bounds__(kThreads, 1)
 dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo,
            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
            const __grid_constant__ CUtensorMap mgk, const __grid_constant__ CUtensorMap mgv, const BwdArgs a) {
   using C = Cfg<D>;
-  constexpr int S = C::kKvStages;
+  constexpr int S = C::kStages, kOut = kCent ? 4 : 2;   // ring slots; those that carry a tile's results
   extern __shared__ uint8_t smem_raw[];
   uint8_t* own = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = own + 2 * C::kOTile;
-  KvExtra<S>& x = *reinterpret_cast<KvExtra<S>*>(ring + S * 2 * C::kSTile);
-  Bars& bar = x.bar;
+  KvExtra& x = *reinterpret_cast<KvExtra*>(ring + S * C::kOTile);
+  KvBars& bar = x.bar;
   volatile int* abort_flag = &x.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntq = (a.nb + 1) / 2, mw = a.mask_words;
-  const int tiles = kCent ? (a.nb + 127) / 128 : ntq;
-  const int tk = blockIdx.x % tiles;
-  const int64_t bh = (blockIdx.x / tiles) % ((int64_t)a.B * a.H), bhs = (int64_t)a.B * a.H;
-  const int split = kCent ? (int)(blockIdx.x / tiles / bhs) : 0;
-  const int b = (int)(bh / a.H), h = (int)(bh % a.H);
+  const int tiles = kCent ? (a.nb + 127) / 128 : ntq;   // of one head (and range)
+  const int64_t bhs = (int64_t)a.B * a.H;
 
   if (tid == 0) {
-    mbar_init(&bar.cent_ready, 1);
-    mbar_init(&bar.own_full, 1 + 256);   // the owned tiles' load, and the softmax threads' zeroed accumulators
-    for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.plan_full[s], 1); mbar_init(&bar.plan_cent[s], 1); mbar_init(&bar.plan_empty[s], 1 + 2 + 8);
+      mbar_init(&bar.own_full[s], 1); mbar_init(&bar.own_free[s], 1);
       mbar_init(&bar.s_full[s], 1); mbar_init(&bar.dp_full[s], 1);
       mbar_init(&bar.p_full[s], 4); mbar_init(&bar.ds_full[s], 4);
+      mbar_init(&bar.acc_full[s], 1); mbar_init(&bar.acc_clear[s], 128);
     }
-    mbar_init(&bar.final_mma, 2);
+    for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
+    mbar_init(&bar.gb_full, 128);
+    mbar_init(&bar.out_full, 8);
+    mbar_init(&bar.plan_go, 1);
+    mbar_init(&bar.mma_done, 2);
     x.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    mbar_expect_tx(&bar.own_full, 2 * C::kOTile);
-    for (int c = 0; c < C::kChunks; ++c) {
-      uint8_t* dk = own + c * C::kOChunk;
-      uint8_t* dv = dk + C::kOTile;
-      if (kCent) {
-        for (int hf = 0; hf < 2; ++hf) {
-          tma_load_3d(dk + hf * (C::kOChunk / 2), &mk, c * 64, 128 * tk + 64 * hf, (int)bh, &bar.own_full);
-          tma_load_3d(dv + hf * (C::kOChunk / 2), &mv, c * 64, 128 * tk + 64 * hf, (int)bh, &bar.own_full);
-        }
-      } else {
-        for (int hf = 0; hf < 2; ++hf) {
-          tma_load_4d(dk + hf * (C::kOChunk / 2), &mk, c * 64, h, 128 * tk + 64 * hf, b, &bar.own_full);
-          tma_load_4d(dv + hf * (C::kOChunk / 2), &mv, c * 64, h, 128 * tk + 64 * hf, b, &bar.own_full);
-        }
-      }
-    }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&x.tmem_base)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (kCent) {
-    // the range's query blocks that leave any of the tile's key blocks to its centroid
-    const int lo = (int)((int64_t)a.nb * split / a.splits), hi = (int)((int64_t)a.nb * (split + 1) / a.splits);
-    if (warp == 2) {
-      int n = 0;
-      for (int i = lo; i < hi; i += 32) {
-        uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        if (i + lane < hi) {
-          const int* P = a.plan + (bh * ntq + ((i + lane) >> 1)) * plan_ints(mw, a.nb) + 16 + ((i + lane) & 1) * mw;
-          for (int e = 0; e < 4; ++e) {
-            const int base = 128 * tk + 32 * e;
-            if (base >= a.nb) continue;
-            w[e] = (uint32_t)P[4 * tk + e];
-            if (a.nb - base < 32) w[e] |= ~((1u << (a.nb - base)) - 1u);
-          }
-        }
-        const bool live = (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu;
-        const uint32_t any = __ballot_sync(0xffffffffu, live);
-        if (live) {
-          const int at = n + __popc(any & ((1u << lane) - 1u));
-          x.list[at] = i + lane;
-          for (int e = 0; e < 4; ++e) x.cword[at][e] = w[e];
-        }
-        n += __popc(any);
-      }
-      if (lane == 0) x.n_steps = n;
-    }
-  } else {
-    const int* P = a.tplan + (bh * ntq + tk) * tplan_ints(a.nb);
-    for (int e = tid; e < a.nb; e += kThreads) x.list[e] = P[16 + e];
-    if (tid == 0) x.n_steps = P[0];
-  }
   fence_before();
   cta_sync();
   fence_after();
   const uint32_t tmem = x.tmem_base;
-  const int T = x.n_steps;
+  auto wait = [&](uint64_t* b, uint32_t par) { return wait_for(b, par & 1u, abort_flag); };
+  auto wait_w = [&](uint64_t* b, uint32_t par) { return __all_sync(0xffffffffu, wait(b, par)) != 0; };
 
   if (warp == 0) {
-    if (lane == 0) {   // Q and dO tiles, -lse and -delta of their rows
-      int nl = 0;
-      for (int t = 0; t < T; ++t) {
-        const int s = t % S, n = t / S, i = x.list[t] & 0xffff;
-        if (!wait_bar(&bar.empty[s], (n & 1) ^ 1, abort_flag, a.status)) break;
-        ++nl;
-        mbar_expect_tx(&bar.full[s], 2 * C::kSTile + 512);
-        load_pair4<D>(ring + s * 2 * C::kSTile, &mq, &mdo, 64 * i, h, b, &bar.full[s]);
-        bulk_load(x.nl[s], a.nlse + (bh * a.nb + i) * 64, 256, &bar.full[s]);
-        bulk_load(x.nd[s], a.ndelta + (bh * a.nb + i) * 64, 256, &bar.full[s]);
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      RingPos<S> pos;
+      int slots = 0, owns = 0;
+      bool ok = true;
+      auto slot = [&]() { return ok = ok && wait(&bar.empty[pos.s], pos.ph ^ 1u); };
+      auto next = [&]() { pos.next(); ++slots; };
+      for (int k = 0;; ++k) {
+        if (!(ok = ok && wait(&bar.plan_full[k & 1], k >> 1))) break;
+        const KvTile& in = x.info[k & 1];
+        if (in.tile < 0) break;
+        const int tk = in.tile % tiles;
+        const int64_t bh = (in.tile / tiles) % bhs;
+        const int h = (int)(bh % a.H), b = (int)(bh / a.H), T = in.n;
+        for (int o = 0; o < 2; ++o) {   // K, V, once the previous tile's products have read theirs
+          if (k > 0 && !(ok = ok && wait(&bar.own_free[o], k - 1))) break;
+          mbar_expect_tx(&bar.own_full[o], C::kOTile);
+          for (int c = 0; c < C::kChunks; ++c)
+            for (int hf = 0; hf < 2; ++hf) {
+              uint8_t* dst = own + o * C::kOTile + c * C::kOChunk + hf * (C::kOChunk / 2);
+              if (kCent) tma_load_3d(dst, o ? &mv : &mk, c * 64, 128 * tk + 64 * hf, (int)bh, &bar.own_full[o]);
+              else tma_load_4d(dst, o ? &mv : &mk, c * 64, h, 128 * tk + 64 * hf, b, &bar.own_full[o]);
+            }
+        }
+        if (!ok) break;
+        ++owns;
+        const int go = max(0, T - kAhead);
+        if (T == 0) mbar_arrive(&bar.plan_go);
+        for (int t = 0; t < T && slot(); ++t, next()) {   // Q and dO, -lse and -delta of their rows
+          if (t == go) mbar_arrive(&bar.plan_go);
+          const int i = in.list[t] & 0xffff;
+          mbar_expect_tx(&bar.full[pos.s], 2 * C::kSTile + 512);
+          load_pair4<D>(ring + pos.s * C::kOTile, &mq, &mdo, 64 * i, h, b, &bar.full[pos.s]);
+          bulk_load(x.nl[pos.s], a.nlse + (bh * a.nb + i) * 64, 256, &bar.full[pos.s]);
+          bulk_load(x.nd[pos.s], a.ndelta + (bh * a.nb + i) * 64, 256, &bar.full[pos.s]);
+        }
+        for (int o = 0; o < kOut && slot(); ++o, next()) mbar_arrive(&bar.full[pos.s]);   // handed over empty
+        if (!ok) break;
+        mbar_arrive(&bar.plan_empty[k & 1]);
       }
-      for (int s = 0; s < S; ++s) {
-        const int cnt = (nl + S - 1 - s) / S;
-        if (cnt) drain_bar(&bar.full[s], (cnt - 1) & 1, a.status);
+      // every armed load has landed before the CTA may exit
+      for (int i = max(0, slots - S); i < slots; ++i) drain_bar(&bar.full[i % S], (i / S) & 1, a.status);
+      if (owns) {
+        drain_bar(&bar.own_full[0], (owns - 1) & 1, a.status);
+        drain_bar(&bar.own_full[1], (owns - 1) & 1, a.status);
       }
-      drain_bar(&bar.own_full, 0, a.status);
     }
   } else if (warp == 1 || warp == 2) {
-    // warp 1: dV += P(t) dO, then S(t+2) over P(t); warp 2: dK += dS(t) Q, then dP(t+2) over dS(t)
+    // ---------------------------------------------------------------- products
+    // warp 1: dV += P(u) dO, then S(u+2) over P(u); warp 2: dK += dS(u) Q, then dP(u+2) over dS(u)
     constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
-    constexpr uint64_t kStep = 2 * (C::kSTile >> 4);   // descriptor step per ring stage
+    constexpr uint64_t kStep = 2 * (C::kSTile >> 4);   // descriptor step per ring slot
     const bool first = warp == 1;
+    const int o = first ? 0 : 1;
     const uint64_t tile = C::kSTile >> 4;
     const uint64_t od = sdesc(smem_u32(own), 16, 1024) + (first ? 0 : C::kOTile >> 4);            // K / V
     const uint64_t sd = sdesc(smem_u32(ring), 16, 1024) + (first ? 0 : tile);                       // Q / dO, K-major
@@ -713,7 +886,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     uint64_t* done = first ? bar.s_full : bar.dp_full;
     uint64_t* ready = first ? bar.p_full : bar.ds_full;
     RingPos<S> ld, use;
-    auto wait_ld = [&]() { return wait_bar(&bar.full[ld.s], ld.ph, abort_flag, a.status); };
+    auto wait_ld = [&]() { return wait(&bar.full[ld.s], ld.ph); };
     auto start = [&](int g, int e) {
       const uint64_t b0 = sd + ld.s * kStep;
       ld.next();
@@ -722,227 +895,351 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         mma_ss_m(col + 128 * g, kmaj<D>(od, kk, C::kOChunk), kmaj<D>(b0, kk, C::kSChunk), id_s, kk > 0 ? 1u : 0u, off(e, 0), off(e, 1));
       mma_commit_w(&done[g]);
     };
-    auto finish = [&](int t, int e) {
+    auto finish = [&](int g, int e) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_ts_m(acc, col + 128 * (t & 1) + kk * 8, gd + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, 1u, off(e, 0), off(e, 1));
+        mma_ts_m(acc, col + 128 * g + kk * 8, gd + use.s * kStep + (uint64_t)(kk * 2048 >> 4), id_g, 1u, off(e, 0), off(e, 1));
       mma_commit_w(&bar.empty[use.s]);
       use.next();
     };
-    // a step's list entry (its halves); centroid tiles take every row
-    auto entry = [&](int t) { return kCent ? 3 << 16 : x.list[t]; };
-    bool ok = __all_sync(0xffffffffu, wait_bar(&bar.own_full, 0, abort_flag, a.status));
-    fence_after();
-    for (int t = 0; t < 2 && t < T && ok; ++t)
-      if ((ok = __all_sync(0xffffffffu, wait_ld()))) start(t, entry(t));
-    int t = 0, e0 = T > 0 ? entry(0) : 0, e1 = T > 1 ? entry(1) : 0, e2 = T > 2 ? entry(2) : 0;   // steps t, t+1, t+2
-    for (; t < T - 2 && ok; ++t) {   // (no condition around a batch: see the last two steps below)
-      ok = wait_ld() && wait_bar(&ready[t & 1], (t >> 1) & 1, abort_flag, a.status);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      fence_after();
-      finish(t, e0);
-      const int e = e2;
-      e0 = e1;
-      e1 = e2;
-      e2 = entry(min(t + 3, T - 1));
-      start(t & 1, e);
-    }
-    for (; t < T && ok; ++t) {
-      if (!(ok = __all_sync(0xffffffffu, wait_bar(&ready[t & 1], (t >> 1) & 1, abort_flag, a.status)))) break;
-      fence_after();
-      finish(t, e0);
-      e0 = e1;
-    }
-    mma_commit_w(&bar.final_mma);
-    if (first) drain_bar(&bar.final_mma, 0, a.status);
-  } else if (!kCent && warp == 3) {
-    // the two blocks' centroid gradients, summed over the query ranges in order (read after the last step)
-    if (a.centroids) {
-#pragma unroll
-      for (int e = lane; e < D; e += 32) {   // float4s of [gk, gv][half][D]
-        const int d = e % (D / 4), half = (e / (D / 4)) & 1, which = e / (D / 2), jj = 2 * tk + half;
-        const float4* src = reinterpret_cast<const float4*>((which ? a.gv : a.gk) + (bh * a.nb + jj) * D) + d;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (jj < a.nb) {
-#pragma unroll 8
-          for (int s = 0; s < a.splits; ++s) {
-            const float4 u = src[s * bhs * a.nb * (D / 4)];
-            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-          }
-        }
-        reinterpret_cast<float4*>(x.gsum[which][half])[d] = v;
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar.cent_ready);
-  } else if (warp >= 4) {
-    const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
-    const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
-    const float sl2 = a.scale * kLog2e;
-    const uint64_t sl22 = f2pack(sl2, sl2);
-    const int j = kCent ? 128 * tk + r : 2 * tk + hf;   // this row's centroid / key block
-    const float cadd = kCent && j < a.nb ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
-    {   // accumulators from zero: group 0 dK, group 1 dV
-      uint32_t z[32];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) z[c] = 0u;
-      for (int c = 0; c < D / 32; ++c) tmem_st32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, z);
-      tmem_wait_st();
-      fence_before();
-      mbar_arrive(&bar.own_full);
-    }
-    uint64_t gb2 = 0ull;   // kCent: the sums of ds of even and odd queries
     bool ok = true;
-    for (int t = g; t < T && ok; t += 2) {
-      const int rs = t % S;
-      bool need = true;
-      uint64_t add2 = 0ull;
-      if (kCent) {
-        const float v = (x.cword[t][sub] >> lane) & 1u ? -INFINITY : cadd;
-        add2 = f2pack(v, v);
-      } else {
-        need = (x.list[t] >> (16 + hf)) & 1;
-      }
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.full[rs], (t / S) & 1, abort_flag, a.status) &&
-                                       wait_bar(&bar.s_full[g], (t >> 1) & 1, abort_flag, a.status));
-      if (!ok) break;
+    int base = 0;   // steps of the earlier tiles
+    for (int k = 0; ok; ++k) {
+      if (!(ok = wait_w(&bar.plan_full[k & 1], k >> 1))) break;
+      const KvTile& in = x.info[k & 1];
+      if (in.tile < 0) break;
+      const int T = in.n;
+      // a step's list entry (its halves); centroid tiles take every row
+      auto entry = [&](int t) { return kCent ? 3 << 16 : in.list[t]; };
+      if (!(ok = wait_w(&bar.own_full[o], k))) break;
+      for (int t = 0; t < 2 && t < T && ok; ++t)
+        if ((ok = __all_sync(0xffffffffu, wait_ld()))) start((base + t) & 1, entry(t));
+      if (!(ok = ok && wait_w(&bar.acc_clear[1 - o], k))) break;
       fence_after();
-      const uint32_t st = lane_addr + C::kStage + 128 * g;
-      float p[64];
-      uint32_t pk[32];
-      if (need) {
-        tmem_ld32(st, p);
-        tmem_ld32(st + 32, p + 32);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float4 l4 = reinterpret_cast<const float4*>(x.nl[rs])[c];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint64_t l2 = u ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y);
-            if (kCent) l2 = fadd2(l2, add2);
-            const int k = 4 * c + 2 * u;
-            float e0, e1;
-            f2unpack(ffma2(f2pack(p[k], p[k + 1]), sl22, l2), e0, e1);
-            p[k] = ex2(e0);
-            p[k + 1] = ex2(e1);
-            pk[2 * c + u] = pack_bf16(p[k], p[k + 1]);
-          }
-        }
-        tmem_st32(st, pk);
-        tmem_wait_st();
+      int u = base, e0 = T > 0 ? entry(0) : 0, e1 = T > 1 ? entry(1) : 0, e2 = T > 2 ? entry(2) : 0;   // steps u, u+1, u+2
+      for (; u < base + T - 2 && ok; ++u) {   // (no condition around a batch: see the last two steps below)
+        ok = wait_ld() && wait(&ready[u & 1], u >> 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        fence_after();
+        finish(u & 1, e0);
+        const int e = e2;
+        e0 = e1;
+        e1 = e2;
+        e2 = entry(min(u + 3 - base, T - 1));
+        start(u & 1, e);
       }
-      fence_before();
+      mma_commit_w(&bar.own_free[o]);
+      for (; u < base + T && ok; ++u) {
+        if (!(ok = wait_w(&ready[u & 1], u >> 1))) break;
+        fence_after();
+        finish(u & 1, e0);
+        e0 = e1;
+      }
+      mma_commit_w(&bar.acc_full[1 - o]);
+      ld.skip(kOut);
+      use.skip(kOut);
+      base += T;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[g]);
-      ok = __all_sync(0xffffffffu, wait_bar(&bar.dp_full[g], (t >> 1) & 1, abort_flag, a.status));
-      if (!ok) break;
-      fence_after();
-      if (need) {
+      if (lane == 0) mbar_arrive(&bar.plan_empty[k & 1]);
+    }
+    mma_commit_w(&bar.mma_done);
+    if (first) drain_bar(&bar.mma_done, 0, a.status);
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- plans, and the results' way out
+    const int64_t total = bhs * tiles * (kCent ? a.splits : 1);
+    auto plan = [&](int k) {   // the next tile off the counter into buffer k & 1
+      KvTile& in = x.info[k & 1];
+      int tile = 0;
+      if (lane == 0) tile = atomicAdd(a.counter + (kCent ? 1 : 2), 1);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
+      if (tile >= total) {
+        if (lane == 0) { in.tile = -1; mbar_arrive(&bar.plan_full[k & 1]); }
+        return;
+      }
+      if (!kCent) tile = tile_at(tile, a.B * a.H, tiles, min(tiles, (a.prefix + 127) / 128));
+      const int tk = tile % tiles;
+      const int64_t bh = (tile / tiles) % bhs;
+      int n = 0;
+      if (kCent) {   // the range's query blocks that leave any of the tile's key blocks to its centroid
+        const int split = (int)(tile / tiles / bhs);
+        const int lo = (int)((int64_t)a.nb * split / a.splits), hi = (int)((int64_t)a.nb * (split + 1) / a.splits);
+        for (int i = lo; i < hi; i += 32) {
+          uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          if (i + lane < hi) {
+            const int* P = a.plan + (bh * ntq + ((i + lane) >> 1)) * plan_ints(mw, a.nb) + 16 + ((i + lane) & 1) * mw;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float dp[32];
-          tmem_ld32(st + 64 + 32 * hh, dp);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 d4 = reinterpret_cast<const float4*>(x.nd[rs])[8 * hh + c];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint64_t n2 = u ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y);
-              const int k = 4 * c + 2 * u;
-              float d0, d1;
-              const uint64_t d2 = fmul2(f2pack(p[32 * hh + k], p[32 * hh + k + 1]), fadd2(f2pack(dp[k], dp[k + 1]), n2));
-              if (kCent) gb2 = fadd2(gb2, d2);
-              f2unpack(d2, d0, d1);
-              pk[16 * hh + 2 * c + u] = pack_bf16(d0, d1);
+            for (int e = 0; e < 4; ++e) {
+              const int first = 128 * tk + 32 * e;
+              if (first >= a.nb) continue;
+              w[e] = (uint32_t)P[4 * tk + e];
+              if (a.nb - first < 32) w[e] |= ~((1u << (a.nb - first)) - 1u);
             }
           }
-        }
-        tmem_st32(st + 64, pk);
-        tmem_wait_st();
-      }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.ds_full[g]);
-    }
-    float gbs, gb_odd;
-    f2unpack(gb2, gbs, gb_odd);
-    gbs += gb_odd;
-    if (kCent && g == 0) x.gb[r] = gbs;
-    if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.final_mma, 0, abort_flag, a.status));
-    if (!kCent && ok) ok = __all_sync(0xffffffffu, wait_bar(&bar.cent_ready, 0, abort_flag, a.status));
-    __syncwarp();
-    if (kCent) bar_sync(1, 256);   // x.gb
-    // Group 0 brings out dk (gk), group 1 dv (gv), through the shared memory that the
-    // tiles no longer need and tile stores.
-    const float sc = g ? 1.f : a.scale;
-    if (ok) {
-      fence_after();
-      if (kCent) {
-        if (g == 1 && j < a.nb) a.gb_[(split * bhs + bh) * a.nb + j] = x.gb[r] + gbs;
-        uint8_t* tile = own + g * (128 * D * 4);
-        for (int c = 0; c < D / 32; ++c) {   // fp32 rows: 32-column chunks of 128 bytes, SW128
-          float v[32];
-          __syncwarp();
-          tmem_ld32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, v);
-          tmem_wait_ld();
+          const bool live = (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu;
+          const uint32_t any = __ballot_sync(0xffffffffu, live);
+          if (live) {
+            const int at = n + __popc(any & ((1u << lane) - 1u));
+            in.list[at] = i + lane;
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<float4*>(tile + c * C::kOChunk + r * 128 + ((u ^ (r & 7)) << 4)) =
-                make_float4(sc * v[4 * u], sc * v[4 * u + 1], sc * v[4 * u + 2], sc * v[4 * u + 3]);
+            for (int e = 0; e < 4; ++e) in.cword[at][e] = w[e];
+          }
+          n += __popc(any);
         }
       } else {
-        const int row = 128 * tk + r;
-        const int64_t plane = bhs * 64 * a.nb, cr = bh * 64 * a.nb + row;
-        float mul = 0.f, beta = 0.f;   // the row's share of its centroid's gradient, and of the anchor's
-        if (row < a.N && a.centroids) {
-          mul = a.mode ? a.coef[(g ? 2 : 0) * plane + cr] : 1.f / (float)min(64, a.N - 64 * j);
-          if (a.mode && g == 0) beta = a.coef[plane + cr];
+        const int* P = a.tplan + (int64_t)tile * tplan_ints(a.nb);
+        n = P[0];
+#pragma unroll 4
+        for (int e = lane; e < n; e += 32) in.list[e] = P[16 + e];
+      }
+      if (lane == 0) { in.tile = tile; in.n = n; }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.plan_full[k & 1]);
+      if (!kCent && a.centroids) {   // the two blocks' centroid gradients, summed over the query ranges in order
+        for (int e = lane; e < D; e += 32) {   // float4s of [gk, gv][half][D]
+          const int d = e % (D / 4), half = (e / (D / 4)) & 1, which = e / (D / 2), jj = 2 * tk + half;
+          const float4* src = reinterpret_cast<const float4*>((which ? a.gv : a.gk) + (bh * a.nb + jj) * D) + d;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (jj < a.nb) {
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s) {
+              const float4 q = src[s * bhs * a.nb * (D / 4)];
+              v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+            }
+          }
+          reinterpret_cast<float4*>(in.gsum[which][half])[d] = v;
         }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.plan_cent[k & 1]);
+    };
+    RingPos<S> pos;
+    plan(0);
+    for (int k = 0;; ++k) {
+      const KvTile& in = x.info[k & 1];
+      if (in.tile < 0) break;
+      if (!wait_w(&bar.plan_go, k) || (k >= 1 && !wait_w(&bar.plan_empty[(k + 1) & 1], ((k + 1) >> 1) - 1))) break;
+      plan(k + 1);
+      pos.skip(in.n);
+      if (!wait_w(&bar.out_full, k)) break;
+      if (lane == 0) {
+        const int tk = in.tile % tiles;
+        const int64_t bh = (in.tile / tiles) % bhs;
+        RingPos<S> q = pos;
+        if (kCent) {
+          const int plane = (int)((in.tile / tiles / bhs) * bhs + bh);
+          for (int o = 0; o < 2; ++o)
+            for (int c = 0; c < D / 32; ++c) {
+              const int at = c * C::kOChunk;
+              RingPos<S> w = q;
+              w.skip(2 * o + at / C::kOTile);
+              tma_store_3d(o ? &mgv : &mgk, 32 * c, 128 * tk, plane, ring + w.s * C::kOTile + at % C::kOTile);
+            }
+          tma_store_wait();
+        } else {
+          const int h = (int)(bh % a.H), b = (int)(bh / a.H);
+          store_rows<D>(&mgk, ring + q.s * C::kOTile, 128 * tk, h, b, a.N);
+          q.next();
+          store_rows<D>(&mgv, ring + q.s * C::kOTile, 128 * tk, h, b, a.N);
+        }
+        for (int o = 0; o < kOut; ++o) {   // (two arrivals free a slot)
+          RingPos<S> w = pos;
+          w.skip(o);
+          mbar_arrive(&bar.empty[w.s]);
+          mbar_arrive(&bar.empty[w.s]);
+        }
+      }
+      pos.skip(kOut);
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax warpgroups
+    const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
+    const uint32_t acc = lane_addr + (g ? C::kDv : C::kDk);   // group 0 brings out dk (gk), group 1 dv (gv)
+    const float sl2 = a.scale * kLog2e, sc = g ? 1.f : a.scale;
+    const uint64_t sl22 = f2pack(sl2, sl2);
+    auto clear = [&](int c) {   // accumulator columns 32c .. from zero
+      uint32_t z[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) z[e] = 0u;
+      tmem_st32(acc + 32 * c, z);
+    };
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) clear(c);
+    tmem_wait_st();
+    fence_before();
+    mbar_arrive(&bar.acc_clear[g]);
+    bool ok = true;
+    int base = 0;   // steps of the earlier tiles
+    RingPos<S> pos;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = wait_w(&bar.plan_full[k & 1], k >> 1))) break;
+      const KvTile& in = x.info[k & 1];
+      if (in.tile < 0) break;
+      const int T = in.n, tk = in.tile % tiles;
+      const int64_t bh = (in.tile / tiles) % bhs;
+      const int j = kCent ? 128 * tk + r : 2 * tk + hf;   // this row's centroid / key block
+      const float cadd = kCent && j < a.nb ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
+      float mul = 0.f, beta = 0.f;   // the row's share of its centroid's gradient, and of the anchor's
+      if (!kCent && a.centroids && 128 * tk + r < a.N) {
+        const int64_t plane = bhs * 64 * a.nb, cr = bh * 64 * a.nb + 128 * tk + r;
+        mul = a.mode ? a.coef[(g ? 2 : 0) * plane + cr] : 1.f / (float)min(64, a.N - 64 * j);
+        if (a.mode && g == 0) beta = a.coef[plane + cr];
+      }
+      uint64_t gb2 = 0ull;   // kCent: the sums of ds of even and odd queries
+      RingPos<S> at = pos;
+      at.skip((base + g) & 1);
+      for (int u = base + ((base + g) & 1); u < base + T; u += 2, at.skip(2)) {   // the steps of this group's stage
+        const int rs = at.s;
+        bool need = true;
+        uint64_t add2 = 0ull;
+        if (kCent) {
+          const float v = (in.cword[u - base][sub] >> lane) & 1u ? -INFINITY : cadd;
+          add2 = f2pack(v, v);
+        } else {
+          need = (in.list[u - base] >> (16 + hf)) & 1;
+        }
+        ok = __all_sync(0xffffffffu, wait(&bar.full[rs], at.ph) && wait(&bar.s_full[g], u >> 1));
+        if (!ok) break;
+        fence_after();
+        const uint32_t st = lane_addr + C::kStage + 128 * g;
+        float p[64];
+        uint32_t pk[32];
+        if (need) {
+          tmem_ld32(st, p);
+          tmem_ld32(st + 32, p + 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float4 l4 = reinterpret_cast<const float4*>(x.nl[rs])[c];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint64_t l2 = q ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y);
+              if (kCent) l2 = fadd2(l2, add2);
+              const int i = 4 * c + 2 * q;
+              float e0, e1;
+              f2unpack(ffma2(f2pack(p[i], p[i + 1]), sl22, l2), e0, e1);
+              p[i] = ex2(e0);
+              p[i + 1] = ex2(e1);
+              pk[2 * c + q] = pack_bf16(p[i], p[i + 1]);
+            }
+          }
+          tmem_st32(st, pk);
+          tmem_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[g]);
+        if (!(ok = wait_w(&bar.dp_full[g], u >> 1))) break;
+        fence_after();
+        if (need) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float dp[32];
+            tmem_ld32(st + 64 + 32 * hh, dp);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 d4 = reinterpret_cast<const float4*>(x.nd[rs])[8 * hh + c];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint64_t n2 = q ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y);
+                const int i = 4 * c + 2 * q;
+                float d0, d1;
+                const uint64_t d2 = fmul2(f2pack(p[32 * hh + i], p[32 * hh + i + 1]), fadd2(f2pack(dp[i], dp[i + 1]), n2));
+                if (kCent) gb2 = fadd2(gb2, d2);
+                f2unpack(d2, d0, d1);
+                pk[16 * hh + 2 * c + q] = pack_bf16(d0, d1);
+              }
+            }
+          }
+          tmem_st32(st + 64, pk);
+          tmem_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ds_full[g]);
+      }
+      if (!ok) break;
+      pos.skip(T);
+      base += T;
+      // the tile's dk (gk) / dv (gv) into its ring slots, from where the planning warp stores it
+      if (!(ok = wait_w(&bar.acc_full[g], k) && wait_w(&bar.plan_cent[k & 1], k >> 1))) break;
+      fence_after();
+      RingPos<S> out = pos;
+      out.skip(g * (kOut / 2));
+      pos.skip(kOut);
+      if (kCent) {
+        float gbs, odd;
+        f2unpack(gb2, gbs, odd);
+        gbs += odd;
+        if (g == 0) {
+          x.gb[k & 1][r] = gbs;
+          mbar_arrive(&bar.gb_full);
+        } else {
+          if (!(ok = wait_w(&bar.gb_full, k))) break;
+          const int64_t split = in.tile / tiles / bhs;
+          if (j < a.nb) a.gb_[(split * bhs + bh) * a.nb + j] = x.gb[k & 1][r] + gbs;
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {   // fp32 rows: 32-column chunks of 128 bytes, SW128
+          const int at = c * C::kOChunk;
+          RingPos<S> q = out;
+          q.skip(at / C::kOTile);
+          if (!(ok = wait_w(&bar.full[q.s], q.ph))) break;
+          uint8_t* row = ring + q.s * C::kOTile + at % C::kOTile + r * 128;
+          float v[32];
+          tmem_ld32(acc + 32 * c, v);
+          tmem_wait_ld();
+          clear(c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(row + ((e ^ (r & 7)) << 4)) = make_float4(sc * v[4 * e], sc * v[4 * e + 1], sc * v[4 * e + 2], sc * v[4 * e + 3]);
+        }
+        if (!ok) break;
+      } else {
+        if (!(ok = wait_w(&bar.full[out.s], out.ph))) break;
         const float4* an = reinterpret_cast<const float4*>(a.anchor + bh * D);
-        const float4* gs = reinterpret_cast<const float4*>(x.gsum[g][hf]);
+        const float4* gs = reinterpret_cast<const float4*>(in.gsum[g][hf]);
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
-          __syncwarp();
-          tmem_ld32(lane_addr + (g ? C::kDv : C::kDk) + 32 * c, v);
+          tmem_ld32(acc + 32 * c, v);
           tmem_wait_ld();
+          clear(c);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] *= sc;
           if (a.centroids) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float4 u = gs[8 * c + e];
-              v[4 * e] = fmaf(mul, u.x, v[4 * e]); v[4 * e + 1] = fmaf(mul, u.y, v[4 * e + 1]);
-              v[4 * e + 2] = fmaf(mul, u.z, v[4 * e + 2]); v[4 * e + 3] = fmaf(mul, u.w, v[4 * e + 3]);
+              const float4 q = gs[8 * c + e];
+              v[4 * e] = fmaf(mul, q.x, v[4 * e]); v[4 * e + 1] = fmaf(mul, q.y, v[4 * e + 1]);
+              v[4 * e + 2] = fmaf(mul, q.z, v[4 * e + 2]); v[4 * e + 3] = fmaf(mul, q.w, v[4 * e + 3]);
             }
             if (a.mode && g == 0) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float4 u = an[8 * c + e];
-                v[4 * e] = fmaf(beta, u.x, v[4 * e]); v[4 * e + 1] = fmaf(beta, u.y, v[4 * e + 1]);
-                v[4 * e + 2] = fmaf(beta, u.z, v[4 * e + 2]); v[4 * e + 3] = fmaf(beta, u.w, v[4 * e + 3]);
+                const float4 q = an[8 * c + e];
+                v[4 * e] = fmaf(beta, q.x, v[4 * e]); v[4 * e + 1] = fmaf(beta, q.y, v[4 * e + 1]);
+                v[4 * e + 2] = fmaf(beta, q.z, v[4 * e + 2]); v[4 * e + 3] = fmaf(beta, q.w, v[4 * e + 3]);
               }
             }
           }
-          put_row<D>(own + g * C::kOTile, r, c, v);
+          put_row<D>(ring + out.s * C::kOTile, r, 2 * c, v);
+          put_row<D>(ring + out.s * C::kOTile, r, 2 * c + 1, v + 16);
         }
       }
+      tmem_wait_st();
       fence_async();
-    }
-    bar_sync(2 + g, 128);
-    if ((tid & 127) == 0 && ok && !*abort_flag) {
-      if (kCent) {
-        for (int c = 0; c < D / 32; ++c)
-          tma_store_3d(g ? &mgv : &mgk, 32 * c, 128 * tk, (int)(split * bhs + bh), own + g * (128 * D * 4) + c * C::kOChunk);
-        tma_store_wait();
-      } else {
-        store_rows<D>(g ? &mgv : &mgk, own + g * C::kOTile, 128 * tk, h, b, a.N);
-      }
+      fence_before();
+      mbar_arrive(&bar.acc_clear[g]);
+      __syncwarp();
+      if (lane == 0) { mbar_arrive(&bar.out_full); mbar_arrive(&bar.plan_empty[k & 1]); }
     }
   }
   fence_before();
   cta_sync();
+  if (tid == 0 && x.abort_flag) raise_status(a.status, SOL_ERR_TIMEOUT);
   if (warp == 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
@@ -1077,12 +1374,11 @@ __global__ void __launch_bounds__(1024) anchor_bwd_kernel(const BwdArgs a) {
 }
 
 template <int D>
-constexpr size_t dq_smem() { return 1024 + Cfg<D>::kDqStages * 2 * Cfg<D>::kSTile + sizeof(DqExtra); }
+constexpr size_t dq_smem() { return 1024 + Cfg<D>::kDqStages * Cfg<D>::kOTile + sizeof(DqExtra); }
 template <int D>
 constexpr size_t dkv_smem() {
-  return 1024 + 2 * Cfg<D>::kOTile + Cfg<D>::kKvStages * 2 * Cfg<D>::kSTile + sizeof(KvExtra<Cfg<D>::kKvStages>);
+  return 1024 + (2 + Cfg<D>::kStages) * Cfg<D>::kOTile + sizeof(KvExtra);
 }
-static_assert(2 * 128 * 128 * 4 <= 2 * Cfg<128>::kOTile + Cfg<128>::kKvStages * 2 * Cfg<128>::kSTile, "fp32 tiles");
 static_assert(dq_smem<128>() <= 232448 && dkv_smem<128>() <= 232448, "shared memory");
 
 // Once per device (so that launches stay free of attribute calls, e.g. inside a
@@ -1144,7 +1440,7 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const unsigned bh = (unsigned)(a.B * a.H), tiles = bh * ((a.nb + 1) / 2);
   if (a.centroids) {
-    dkv_kernel<D, true><<<bh * ((a.nb + 127) / 128) * a.splits, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mkb, mvb, mgk, mgv, a);
+    dkv_kernel<D, true><<<std::min(bh * ((a.nb + 127) / 128) * a.splits, kSms), kThreads, dkv_smem<D>(), st>>>(mq, mdo, mkb, mvb, mgk, mgv, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (a.centroids && a.mode) {
@@ -1153,9 +1449,9 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
     anchor_bwd_kernel<D><<<a.B * a.H, 1024, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  dq_kernel<D><<<tiles, kThreads, dq_smem<D>(), st>>>(mq, mdo, mdq, mk, mv, mkb, mvb, a);
+  dq_kernel<D><<<std::min(tiles, kSms), kThreads, dq_smem<D>(), st>>>(mq, mdo, mdq, mk, mv, mkb, mvb, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  dkv_kernel<D, false><<<tiles, kThreads, dkv_smem<D>(), st>>>(mq, mdo, mk, mv, mdk, mdv, a);
+  dkv_kernel<D, false><<<std::min(tiles, kSms), kThreads, dkv_smem<D>(), st>>>(mq, mdo, mk, mv, mdk, mdv, a);
   return cudaGetLastError();
 }
 

@@ -195,6 +195,7 @@ struct BwdArgs {
   float* coef;                   // [3][BH][64 nb]: alpha, beta, gamma of each key row (modes 1, 2)
   float* da_part;                // [BH][nb][D] (modes 1, 2)
   float* da;                     // [BH][D] anchor gradient over its row count (modes 1, 2)
+  int* counter;                  // [4] tile counters of the persistent passes
   int* status;
 };
 int attn_bwd_splits(int nb);
