@@ -52,9 +52,10 @@ __global__ void __launch_bounds__(256) stat_kernel(const BwdArgs a) {
   __shared__ float sd[kStatHeads][65];
   const int hg = (a.H + kStatHeads - 1) / kStatHeads, blk = blockIdx.x / hg % a.nb;
   const int b = blockIdx.x / hg / a.nb, h0 = (int)(blockIdx.x % hg) * kStatHeads;
+  griddep_launch();   // the plans do not depend on this
   if (blockIdx.x == 0 && threadIdx.x < 4) a.counter[threadIdx.x] = 0;   // the later passes' tile counters
   const int c = threadIdx.x % LPR, g = threadIdx.x / LPR;
-#pragma unroll 4
+#pragma unroll 8
   for (int e = g; e < 64 * kStatHeads; e += G) {   // heads fastest: contiguous rows of BTHD
     const int hh = e % kStatHeads, r = e / kStatHeads, n = 64 * blk + r, h = h0 + hh;
     uint4 x = make_uint4(0, 0, 0, 0), y = x;
@@ -98,6 +99,8 @@ __global__ void __launch_bounds__(kTWarps * 32) tplan_kernel(const BwdArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, m = blockIdx.y;
   const int64_t bh = blockIdx.x;
   const int ntq = (a.nb + 1) / 2, qw = (a.nb + 31) / 32, pi = plan_ints(a.mask_words, a.nb);
+  griddep_launch();
+  griddep_wait();
   for (int w = warp; w < qw; w += kTWarps) {
     const int i = 32 * w + lane;
     uint32_t bits = 0u;
@@ -255,6 +258,7 @@ struct KvTile {
   int list[kMaxKeyBlocks];                        // query blocks: i | needA << 16 | needB << 17
   uint32_t cword[128][4];                         // centroids: each step's exact-block bits of the tile
   alignas(16) float gsum[2][2][128];              // exact: the two blocks' gk, gv
+  float coef[3][128];                             // and the rows' alpha, beta, gamma
 };
 struct KvBars {
   uint64_t plan_full[2], plan_cent[2], plan_empty[2];   // a buffer's list / centroid sums are there; all roles are done
@@ -368,6 +372,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntq = (a.nb + 1) / 2, mw = a.mask_words;
 
+  griddep_launch();   // the next pass may take up idle SMs
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.plan_full[s], 1); mbar_init(&bar.plan_cent[s], 1); mbar_init(&bar.plan_empty[s], 1 + 2 + 8);
@@ -737,6 +742,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
       fence_after();
       const int row = 128 * (tile % ntq) + r;
       const bool anch = a.da && (row >= a.prefix || a.prefix == a.N);
+      if (a.da && k == 0) griddep_wait();   // launched early: the anchor's gradient has to be there from here on
       const float4* da = reinterpret_cast<const float4*>(a.da + (int64_t)(tile / ntq) * D);
 #pragma unroll 1
       for (int c = g; c < D / 16; c += 2) {
@@ -767,6 +773,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
   fence_before();
   cta_sync();
   if (tid == 0 && x.abort_flag) raise_status(a.status, SOL_ERR_TIMEOUT);
+  griddep_wait();   // not complete before the pass in front of it
   if (warp == 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
@@ -796,6 +803,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
   const int tiles = kCent ? (a.nb + 127) / 128 : ntq;   // of one head (and range)
   const int64_t bhs = (int64_t)a.B * a.H;
 
+  if (kCent) griddep_wait();   // the plans and row statistics: the passes after this one rely on them without a wait
+  griddep_launch();            // the next pass may take up idle SMs
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.plan_full[s], 1); mbar_init(&bar.plan_cent[s], 1); mbar_init(&bar.plan_empty[s], 1 + 2 + 8);
@@ -994,6 +1003,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (lane == 0) { in.tile = tile; in.n = n; }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.plan_full[k & 1]);
+      if (!kCent && k == 0) griddep_wait();   // launched early: the centroids' pass has to be complete from here on
       if (!kCent && a.centroids) {   // the two blocks' centroid gradients, summed over the query ranges in order
         for (int e = lane; e < D; e += 32) {   // float4s of [gk, gv][half][D]
           const int d = e % (D / 4), half = (e / (D / 4)) & 1, which = e / (D / 2), jj = 2 * tk + half;
@@ -1007,6 +1017,15 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
             }
           }
           reinterpret_cast<float4*>(in.gsum[which][half])[d] = v;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // the rows' coefficients alpha, beta, gamma
+          const int row = 128 * tk + 32 * q + lane, jj = row >> 6;
+          const int64_t plane = bhs * 64 * a.nb, at = bh * 64 * a.nb + row;
+          const float even = 1.f / (float)min(64, max(1, a.N - 64 * jj));
+#pragma unroll
+          for (int o = 0; o < 3; ++o)
+            in.coef[o][32 * q + lane] = row >= a.N ? 0.f : a.mode ? a.coef[o * plane + at] : o == 1 ? 0.f : even;
         }
       }
       __syncwarp();
@@ -1080,12 +1099,6 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       const int64_t bh = (in.tile / tiles) % bhs;
       const int j = kCent ? 128 * tk + r : 2 * tk + hf;   // this row's centroid / key block
       const float cadd = kCent && j < a.nb ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
-      float mul = 0.f, beta = 0.f;   // the row's share of its centroid's gradient, and of the anchor's
-      if (!kCent && a.centroids && 128 * tk + r < a.N) {
-        const int64_t plane = bhs * 64 * a.nb, cr = bh * 64 * a.nb + 128 * tk + r;
-        mul = a.mode ? a.coef[(g ? 2 : 0) * plane + cr] : 1.f / (float)min(64, a.N - 64 * j);
-        if (a.mode && g == 0) beta = a.coef[plane + cr];
-      }
       uint64_t gb2 = 0ull;   // kCent: the sums of ds of even and odd queries
       RingPos<S> at = pos;
       at.skip((base + g) & 1);
@@ -1199,6 +1212,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         if (!ok) break;
       } else {
         if (!(ok = wait_w(&bar.full[out.s], out.ph))) break;
+        // the row's share of its centroid's gradient, and of the anchor's
+        const float mul = in.coef[g ? 2 : 0][r], beta = in.coef[1][r];
         const float4* an = reinterpret_cast<const float4*>(a.anchor + bh * D);
         const float4* gs = reinterpret_cast<const float4*>(in.gsum[g][hf]);
 #pragma unroll 1
@@ -1240,6 +1255,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
   fence_before();
   cta_sync();
   if (tid == 0 && x.abort_flag) raise_status(a.status, SOL_ERR_TIMEOUT);
+  griddep_wait();   // not complete before the pass in front of it
   if (warp == 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
@@ -1260,6 +1276,7 @@ __global__ void __launch_bounds__(256) pool_bwd_kernel(const BwdArgs a) {
   const int64_t bh = blockIdx.x, bhs = (int64_t)a.B * a.H;
   const int b = (int)(bh / a.H), h = (int)(bh % a.H);
   const int c = threadIdx.x % LPR, g = threadIdx.x / LPR, n = min(64, a.N - 64 * j);
+  griddep_launch();
   uint4 kr[R], vr[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -1269,6 +1286,7 @@ __global__ void __launch_bounds__(256) pool_bwd_kernel(const BwdArgs a) {
     if (r < n) kr[i] = *reinterpret_cast<const uint4*>(a.k + at);
     if (r < n && a.mode == 2) vr[i] = *reinterpret_cast<const uint4*>(a.v + at);
   }
+  griddep_wait();   // the centroids' pass (K and V above need nothing of it)
   // the block's gk and gv, summed over the query ranges in order (one dim of one of them a thread)
   for (int e = threadIdx.x; e < 2 * D; e += 256) {
     const float* src = (e < D ? a.gk : a.gv) + (bh * a.nb + j) * D + e % D;
@@ -1361,6 +1379,8 @@ __global__ void __launch_bounds__(1024) anchor_bwd_kernel(const BwdArgs a) {
   __shared__ float red[K][D];
   const int64_t bh = blockIdx.x;
   const int d = threadIdx.x % D, s = threadIdx.x / D;
+  griddep_launch();
+  griddep_wait();
   float v = 0.f;
   for (int j = s; j < a.nb; j += K) v += a.da_part[(bh * a.nb + j) * D + d];
   red[s][d] = v;
@@ -1430,38 +1450,43 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   cudaError_t e = prepare<D>();
   if (e != cudaSuccess) return e;
-  stat_kernel<D><<<(unsigned)(a.B * a.nb) * ((a.H + kStatHeads - 1) / kStatHeads), 256, 0, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // Every launch but the first may overlap the one before it.  Who waits for what:
+  // the plans need nothing of stat_kernel; tplan_kernel waits for the plans, the
+  // centroids' pass for both; behind that pass nothing starts before it has these.
+  // Then dQ's pass waits only for the anchor's gradient (modes 1, 2), at a tile's end,
+  // and the keys' pass for the centroids' sums, at a tile's end.  Each kernel waits
+  // for the one before it before it is complete, so the chain ends in order.
+  e = launch_kernel(stat_kernel<D>, (unsigned)(a.B * a.nb) * ((a.H + kStatHeads - 1) / kStatHeads), 256, 0, st, false, a);
+  if (e != cudaSuccess) return e;
   AttnArgs pa{};
   pa.row_ptr = a.row_ptr; pa.col_idx = a.col_idx; pa.plan = a.plan; pa.status = a.status;
   pa.B = a.B; pa.H = a.H; pa.N = a.N; pa.nqb = pa.nkb = a.nb; pa.centroids = a.centroids;
-  if ((e = launch_plan(pa, st)) != cudaSuccess) return e;
-  tplan_kernel<<<dim3(a.B * a.H, a.mask_words), kTWarps * 32, 0, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_plan(pa, st, true)) != cudaSuccess) return e;
   const unsigned bh = (unsigned)(a.B * a.H), tiles = bh * ((a.nb + 1) / 2);
+  if ((e = launch_kernel(tplan_kernel, dim3(bh, a.mask_words), kTWarps * 32, 0, st, true, a)) != cudaSuccess) return e;
   if (a.centroids) {
-    dkv_kernel<D, true><<<std::min(bh * ((a.nb + 127) / 128) * a.splits, kSms), kThreads, dkv_smem<D>(), st>>>(mq, mdo, mkb, mvb, mgk, mgv, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const unsigned n = std::min(bh * ((a.nb + 127) / 128) * a.splits, kSms);
+    e = launch_kernel(dkv_kernel<D, true>, n, kThreads, dkv_smem<D>(), st, true, mq, mdo, mkb, mvb, mgk, mgv, a);
+    if (e != cudaSuccess) return e;
+    if (a.mode) {
+      if ((e = launch_kernel(pool_bwd_kernel<D>, dim3(bh, a.nb), 256, 0, st, true, a)) != cudaSuccess) return e;
+      if ((e = launch_kernel(anchor_bwd_kernel<D>, bh, 1024, 0, st, true, a)) != cudaSuccess) return e;
+    }
   }
-  if (a.centroids && a.mode) {
-    pool_bwd_kernel<D><<<dim3(a.B * a.H, a.nb), 256, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    anchor_bwd_kernel<D><<<a.B * a.H, 1024, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  dq_kernel<D><<<std::min(tiles, kSms), kThreads, dq_smem<D>(), st>>>(mq, mdo, mdq, mk, mv, mkb, mvb, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  dkv_kernel<D, false><<<std::min(tiles, kSms), kThreads, dkv_smem<D>(), st>>>(mq, mdo, mk, mv, mdk, mdv, a);
-  return cudaGetLastError();
+  e = launch_kernel(dq_kernel<D>, std::min(tiles, kSms), kThreads, dq_smem<D>(), st, a.centroids != 0, mq, mdo, mdq, mk, mv, mkb, mvb, a);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(dkv_kernel<D, false>, std::min(tiles, kSms), kThreads, dkv_smem<D>(), st, true, mq, mdo, mk, mv, mdk, mdv, a);
 }
 
 }  // namespace
 
 // Query ranges of the centroid pass.  By the length alone, so that a head's
-// result does not depend on how many heads a call has; sixteen query blocks a
-// range keep short sequences' CTAs many, eight ranges at most bound the partial
-// sums' memory.
-int attn_bwd_splits(int nb) { return nb <= 16 ? 1 : nb >= 128 ? 8 : (nb + 15) / 16; }
+// result does not depend on how many heads a call has.  Up to 32 blocks, where few
+// CTAs are at work and a call is as long as one range, four query blocks a range
+// (N = 1024, H = 2, D = 64: 11.4 us against 19.7 in one range); beyond, sixteen, which
+// is what a tile's way in and out costs (N = 4096, H = 56: 43 us against 61 with
+// eight), and at most eight ranges for the partial sums' memory.
+int attn_bwd_splits(int nb) { return nb <= 32 ? (nb + 3) / 4 : std::min(8, (nb + 15) / 16); }
 
 cudaError_t launch_attn_bwd(const BwdArgs& a, int D, cudaStream_t st) {
   return D == 128 ? launch<128>(a, st) : launch<64>(a, st);

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const AttnArgs a,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntq = (a.nqb + 1) / 2;
   const int64_t tile = (int64_t)blockIdx.x * kPlanWarps + warp;
+  griddep_launch();
   if (tile >= (int64_t)a.B * a.H * ntq) return;   // whole warp
   const int tq = (int)(tile % ntq);
   const int64_t bh = tile / ntq;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const AttnArgs a,
     P[12] = a.centroids ? (int)wa0 : 0;   // bitmap words with a block unselected by the first / second block
     P[13] = a.centroids ? (int)wa1 : 0;
   }
+  griddep_wait();   // launched early: not complete before the kernel in front of it
 }
 
 template <int D, bool I8>
@@ -1012,10 +1014,10 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_plan(const AttnArgs& a, cudaStream_t st) {
+cudaError_t launch_plan(const AttnArgs& a, cudaStream_t st, bool early) {
   const int64_t tiles = (int64_t)a.B * a.H * ((a.nqb + 1) / 2);
-  plan_kernel<<<(unsigned)((tiles + kPlanWarps - 1) / kPlanWarps), kPlanWarps * 32, 0, st>>>(a, (a.nkb + 31) / 32);
-  return cudaGetLastError();
+  return launch_kernel(plan_kernel, (unsigned)((tiles + kPlanWarps - 1) / kPlanWarps), kPlanWarps * 32, 0, st, early, a,
+                       (a.nkb + 31) / 32);
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int D, cudaStream_t st) {

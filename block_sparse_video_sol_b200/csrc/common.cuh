@@ -159,8 +159,9 @@ size_t reblock_axis_floats(int BH, int n_v, int D);        // size of ReblockArg
 cudaError_t launch_reblock(const ReblockArgs& a, int iters, cudaStream_t st);
 cudaError_t launch_rows(const int32_t* perm, const __nv_bfloat16* src, __nv_bfloat16* dst, int B, int H, int N, int D,
                         int64_t sb, int64_t sn, int64_t sh, bool gather, int* status, cudaStream_t st);
-// The per-tile attention plans (plan_kernel) of a.row_ptr / a.col_idx into a.plan.
-cudaError_t launch_plan(const AttnArgs& a, cudaStream_t st);
+// The per-tile attention plans (plan_kernel) of a.row_ptr / a.col_idx into a.plan; `early`: the
+// launch may overlap the kernel before it (which must not touch what the plans read or write).
+cudaError_t launch_plan(const AttnArgs& a, cudaStream_t st, bool early = false);
 #ifdef SOL_FAULT_TEST
 cudaError_t set_drop_p_arrive(int step);   // fault-test build only
 #endif
