@@ -141,8 +141,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without the Stream object (0.3 us against 3.2, of a 10 us call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def sol_workspace_bytes(p: sol_params) -> int:
