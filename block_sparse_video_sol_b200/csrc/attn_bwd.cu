@@ -1005,6 +1005,14 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (lane == 0) { in.tile = tile; in.n = n; }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.plan_full[k & 1]);
+    };
+    // The tile's centroid sums: wanted at its end only, so they are read after the
+    // previous tile's results are stored (which the loads' ring waits for).
+    auto plan_cent = [&](int k) {
+      KvTile& in = x.info[k & 1];
+      if (in.tile < 0) return;
+      const int tk = in.tile % tiles;
+      const int64_t bh = (in.tile / tiles) % bhs;
       if (!kCent && k == 0) griddep_wait();   // launched early: the centroids' pass has to be complete from here on
       if (!kCent && a.centroids) {   // the two blocks' centroid gradients, summed over the query ranges in order
         for (int e = lane; e < D; e += 32) {   // float4s of [gk, gv][half][D]
@@ -1035,6 +1043,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     };
     RingPos<S> pos;
     plan(0);
+    plan_cent(0);
     for (int k = 0;; ++k) {
       const KvTile& in = x.info[k & 1];
       if (in.tile < 0) break;
@@ -1071,6 +1080,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       }
       pos.skip(kOut);
       __syncwarp();
+      plan_cent(k + 1);
     }
   } else {
     // ---------------------------------------------------------------- softmax warpgroups
@@ -1466,6 +1476,11 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   // Then dQ's pass waits only for the anchor's gradient (modes 1, 2), at a tile's end,
   // and the keys' pass for the centroids' sums, at a tile's end.  Each kernel waits
   // for the one before it before it is complete, so the chain ends in order.
+  // The keys' plan and the pooling start early only where the pooling's CTAs, one a
+  // key block, are resident at once (four an SM): queued behind the pass in front
+  // they lose more than a launch's latency (modes 1, 2; N = 1000, B = 2, H = 3: 48 us
+  // early, 52 not; N = 8192, H = 56, 20% of the blocks: 2045 early, 1980 not).
+  const bool few = (unsigned)(a.B * a.H) * a.nb <= 4 * kSms;
   e = launch_kernel(stat_kernel<D>, (unsigned)(a.B * a.nb) * (64 / kStatRows) * ((a.H + kStatHeads - 1) / kStatHeads), 256, 0, st, false, a);
   if (e != cudaSuccess) return e;
   AttnArgs pa{};
@@ -1473,13 +1488,13 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   pa.B = a.B; pa.H = a.H; pa.N = a.N; pa.nqb = pa.nkb = a.nb; pa.centroids = a.centroids;
   if ((e = launch_plan(pa, st, true)) != cudaSuccess) return e;
   const unsigned bh = (unsigned)(a.B * a.H), tiles = bh * ((a.nb + 1) / 2);
-  if ((e = launch_kernel(tplan_kernel, dim3(bh, a.mask_words), kTWarps * 32, 0, st, true, a)) != cudaSuccess) return e;
+  if ((e = launch_kernel(tplan_kernel, dim3(bh, a.mask_words), kTWarps * 32, 0, st, few, a)) != cudaSuccess) return e;
   if (a.centroids) {
     const unsigned n = std::min(bh * ((a.nb + 127) / 128) * a.splits, kSms);
     e = launch_kernel(dkv_kernel<D, true>, n, kThreads, dkv_smem<D>(), st, true, mq, mdo, mkb, mvb, mgk, mgv, a);
     if (e != cudaSuccess) return e;
     if (a.mode) {
-      if ((e = launch_kernel(pool_bwd_kernel<D>, dim3(bh, a.nb), 256, 0, st, true, a)) != cudaSuccess) return e;
+      if ((e = launch_kernel(pool_bwd_kernel<D>, dim3(bh, a.nb), 256, 0, st, few, a)) != cudaSuccess) return e;
       if ((e = launch_kernel(anchor_bwd_kernel<D>, bh, 1024, 0, st, true, a)) != cudaSuccess) return e;
     }
   }
