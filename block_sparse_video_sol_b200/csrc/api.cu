@@ -593,7 +593,15 @@ sol_status sol_qk_norm_rope_bwd(const sol_params* p, const sol_norm_rope* nr, co
   sol_status s = validate(p);
   if (s != SOL_OK) return s;
   if ((s = check_norm_rope(p, nr, "sol_qk_norm_rope_bwd")) != SOL_OK) return s;
-  if (empty(p)) return SOL_OK;
+  if (empty(p)) {   // no rows: the weights' gradients are sums of nothing
+    if (!dq_weight && !dk_weight) return SOL_OK;
+    if ((s = check_arch()) != SOL_OK) return s;
+    for (float* w : {dq_weight, dk_weight}) {
+      const cudaError_t e = w ? cudaMemsetAsync(w, 0, (size_t)p->D * 4, static_cast<cudaStream_t>(stream)) : cudaSuccess;
+      if (e != cudaSuccess) return cuda_fail(e, "sol_qk_norm_rope_bwd memset");
+    }
+    return SOL_OK;
+  }
   if (!q || !k || !dqo || !dko || !dq || !dk || !ws) return fail(SOL_ERR_INVALID_ARG, "sol_qk_norm_rope_bwd: NULL pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(dqo) || !aligned16(dko) || !aligned16(dq) || !aligned16(dk) ||
       !aligned16(dq_weight) || !aligned16(dk_weight))

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256) stat_kernel(const BwdArgs a) {
     float nl = -INFINITY, nd = 0.f;
     if (n < a.N) {
       const float l = a.lse[bh * a.N + n];
-      if (l > -INFINITY) { nl = -l * kLog2e; nd = -sd[hh][r]; }   // a row without keys: p = 0 everywhere
+      if (l != -INFINITY) { nl = -l * kLog2e; nd = -sd[hh][r]; }   // a row without keys: p = 0 everywhere; NaN stays NaN
     }
     a.nlse[at] = nl;
     a.ndelta[at] = nd;

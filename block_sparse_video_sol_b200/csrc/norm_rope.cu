@@ -134,12 +134,13 @@ __device__ __forceinline__ void partners(const uint4& u, int partner, uint64_t* 
   }
 }
 
-// The work is cut into jobs (t, b, n, part): one of Q / K, one position, one of
-// `parts` runs of its head chunks (kHeads heads per lane group each).  Job w of
-// the W warps' first round is warp w's, and every further one W jobs on, so that
-// all warps read and write in one moving window (ranges of their own, one per
-// warp, spread the accesses over every page of the tensors at once).  The job
-// index is kept in digits and stepped by W's digits: no division per job.
+// The work is cut into jobs (t, b, n, part): one of Q / K, one position, and all
+// its head chunks (kHeads heads per lane group each; parts = 1) or one of them
+// (parts = chunks).  Job w of the W warps' first round is warp w's, and every
+// further one W jobs on, so that all warps read and write in one moving window
+// (ranges of their own, one per warp, spread the accesses over every page of the
+// tensors at once).  The job index is kept in digits and stepped by W's digits: no
+// division per job.
 struct Grid {
   int chunks, parts, N, B;
 };
@@ -161,8 +162,8 @@ struct Pos {
     open(g);
   }
   __device__ __forceinline__ void open(const Grid& g) {
-    chunk = p * g.chunks / g.parts;
-    end = (p + 1) * g.chunks / g.parts;
+    chunk = g.parts == 1 ? 0 : p;
+    end = g.parts == 1 ? g.chunks : p + 1;
   }
   // to the next head chunk; true at a new job
   __device__ __forceinline__ bool next(const Grid& g) {

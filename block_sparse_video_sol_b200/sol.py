@@ -261,8 +261,9 @@ def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Te
     """
     weights = [w for w in (q_weight, k_weight) if w is not None]
     for w in weights:
-        if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != weights[0].dtype or not w.is_contiguous():
-            raise ValueError("the weights must be contiguous, both fp32 or both bf16")
+        if (w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != weights[0].dtype or not w.is_contiguous()
+                or w.dim() != 1 or w.shape != weights[0].shape):
+            raise ValueError("the weights must be contiguous, of one length, both fp32 or both bf16")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     sb = sn = 0
@@ -285,11 +286,21 @@ def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Te
                        float(eps), int(rot_dim), int(bool(interleaved)), _ptr(cos) if rot_dim else None,
                        _ptr(sin) if rot_dim else None, sb, sn)
     nr.tensors = (q_weight, k_weight, cos, sin)
+    # what they cover: head dims, positions, batch entries (None: any)
+    nr.covers = (weights[0].shape[0] if weights else None, cos.shape[-2] if rot_dim else None,
+                 cos.shape[0] if rot_dim and cos.dim() == 3 and cos.shape[0] > 1 else None)
     return nr
+
+
+def _check_covers(p: sol_params, nr: sol_norm_rope):
+    D, N, B = getattr(nr, "covers", (None, None, None))   # a structure filled by hand has none
+    if (D is not None and D != p.D) or (N is not None and N < p.N) or (B is not None and B < p.B):
+        raise ValueError(f"weights of {D} dims and tables of {B} x {N} positions do not cover B={p.B}, N={p.N}, D={p.D}")
 
 
 def sol_qk_norm_rope(p: sol_params, nr: sol_norm_rope, q, k, qo, ko, stream=None):
     """RMS norm per head and position rotation of q and k (p's in_strides) into qo and ko (p's out_strides)."""
+    _check_covers(p, nr)
     _check(lib.sol_qk_norm_rope(ctypes.byref(p), ctypes.byref(nr), _ptr(q), _ptr(k), _ptr(qo), _ptr(ko),
                                 _stream(stream)), "sol_qk_norm_rope")
 
@@ -302,6 +313,7 @@ def sol_qk_norm_rope_bwd(p: sol_params, nr: sol_norm_rope, q, k, dqo, dko, dq, d
                          dk_weight: Optional[torch.Tensor], ws: torch.Tensor, grad_strides=None, stream=None):
     """Gradient of sol_qk_norm_rope: dqo, dko (p's out_strides) into dq, dk (``grad_strides``, or p's
     in_strides) and the fp32 weight gradients (each may be None)."""
+    _check_covers(p, nr)
     _check(lib.sol_qk_norm_rope_bwd(ctypes.byref(p), ctypes.byref(nr), _ptr(q), _ptr(k), _ptr(dqo), _ptr(dko),
                                     _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _strides3(grad_strides),
                                     _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
@@ -446,7 +458,8 @@ def backward_reblocked(p: sol_params, rb: ReblockBuffers, d_o: torch.Tensor, g: 
     if rb.buf.lse is None:
         raise ValueError("the backward pass needs the forward's lse (alloc_reblock(with_lse=True))")
     hm = (p.H * p.N * p.D, p.D, p.N * p.D)
-    dop, dqp, dkp, dvp = (torch.empty_like(rb.qp) for _ in range(4))
+    with torch.cuda.stream(stream):   # memory of the stream that uses it
+        dop, dqp, dkp, dvp = (torch.empty_like(rb.qp) for _ in range(4))
     sol_gather_rows(p, rb.perm, d_o, dop, stream)
     sol_attn_bwd(rb.hm, rb.qp, rb.kp, rb.vp, rb.buf.ws, rb.buf.row_ptr, rb.buf.col_idx, rb.buf.o, rb.buf.lse, dop, dqp,
                  dkp, dvp, g.ws, hm, stream)
@@ -495,7 +508,11 @@ def differentiable_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
                              log_mass_bias: int = 0, scale: float = 0.0, topk_ratio: Optional[float] = None,
                              compressed: bool = False) -> torch.Tensor:
     """``attention`` for autograd: returns o [B, N, H, D], whose backward runs sol_attn_bwd on the
-    forward's lists.  The workspace and lists of the call are kept until the backward pass."""
+    forward's lists.  The workspace and lists of the call are kept until the backward pass.
+
+    A step with its backward pass can be captured into a graph.  Its leaves must then be new in the
+    capture (``q.detach().requires_grad_()``) if an earlier eager graph of them is alive: their
+    gradients' accumulation belongs to that graph's stream, which a capture may not wait on."""
     _check_bthd((q, k, v), "q, k, v")
     B, N, H, D = q.shape
     p = make_params(B, N, H, D, tau, prefix_len, log_mass_bias, scale, in_strides=q.stride()[:3],
@@ -538,7 +555,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     """RMS norm of every query and key head and the position rotation, for autograd.
 
     q, k are bf16 CUDA tensors [B, N, H, D] (views of the fused projection allowed); weights and
-    tables as for make_norm_rope.  Returns new contiguous (q, k)."""
+    tables as for make_norm_rope; the tables have no gradient.  Returns new contiguous (q, k).
+    Captured into a graph like ``differentiable_attention``."""
+    if any(t is not None and t.requires_grad for t in (cos, sin)):
+        raise ValueError("the tables have no gradient: cos and sin must not require one")
     _check_bthd((q, k), "q, k")
     B, N, H, D = q.shape
     for w in (q_weight, k_weight):

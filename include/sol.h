@@ -312,17 +312,22 @@ sol_status sol_scatter_rows(const sol_params* p, const int32_t* perm, const void
  *            strides p->out_stride_* (0 repeats, e.g. an expanded gradient).
  *   dq, dk, dv  bf16 device, written (rows < N): strides g_strides[3] = {b, n,
  *            h} in elements, or p->in_stride_* if g_strides is NULL.  Every
- *            (b, n, h) must be a row of its own, or SOL_ERR_INVALID_ARG.
+ *            (b, n, h) must be a row of its own (taken by size, each stride
+ *            clears what the smaller ones span), or SOL_ERR_INVALID_ARG.  They
+ *            must not overlap one another or an input.
  *   bws      device workspace of bws_bytes >= sol_attn_bwd_workspace_bytes(p),
- *            256-byte aligned; nothing in it outlives the call.
+ *            256-byte aligned; nothing in it outlives the call.  Calls that may
+ *            run at once (two streams, two captured graphs) each need their own;
+ *            ws, which is only read, may be shared.
  * The gradient runs through the exact terms and through the centroid terms
  * into the rows that were pooled: block means (log_mass_bias 0), the
  * log-mass bias and its anchor (1), the weighted summaries (2); the rounding of
  * the centroids to bf16 is passed straight through.  A row whose lists are
- * empty and that has no centroid terms (routing 1) gets dq = 0.  A non-finite
- * row of K or V reaches every query row of a 128-row tile that takes its key
- * block, as in sol_attn_fwd; one of Q or dO every key row of a 128-row tile.
- * No atomics: the same inputs give the same bits.  qk_int8 = 1:
+ * empty and that has no centroid terms (routing 1) gets dq = 0, and its o and
+ * lse are not used.  Non-finite values go where the formula takes them, given o
+ * and lse (which sol_attn_fwd makes non-finite for every row of a 128-row tile
+ * that takes a non-finite key block).  No sum is made by atomics: the same inputs
+ * give the same bits, whatever else a call holds.  qk_int8 = 1:
  * SOL_ERR_UNSUPPORTED (its codes have no gradient). */
 size_t sol_attn_bwd_workspace_bytes(const sol_params* p);
 sol_status sol_attn_bwd(const sol_params* p, const void* q, const void* k, const void* v, const void* ws,
@@ -347,7 +352,8 @@ typedef struct {
 /* sol_qk_norm_rope: RMS norm of every query and key head and the position
  * rotation in one pass.  Per row x: y = x / sqrt(mean x^2 + eps) * weight, then
  * the pairs (a, b) of the turned dims become (a cos - b sin, b cos + a sin);
- * fp32 inside, rounded once.
+ * fp32 inside, rounded once (values past 1e18 overflow the mean square, and their
+ * row becomes zeros).
  *   q, k     [B, N, H, D] bf16, strides p->in_stride_* (e.g. views of the fused
  *            QKV projection);  qo, ko  the same shape, strides p->out_stride_*,
  *            distinct rows.  qo = q and ko = k in place is allowed with equal
@@ -366,7 +372,8 @@ sol_status sol_qk_norm_rope(const sol_params* p, const sol_norm_rope* nr, const 
  *            NULL.
  *   ws       device workspace, 256-byte aligned, of at least
  *            sol_qk_norm_rope_bwd_workspace_bytes(p) bytes.
- * The weights' gradients are summed in a fixed order. */
+ * The weights' gradients are summed in a fixed order; they are zeros if B or N
+ * is 0.  As above, calls that may run at once need workspaces of their own. */
 size_t sol_qk_norm_rope_bwd_workspace_bytes(const sol_params* p);
 sol_status sol_qk_norm_rope_bwd(const sol_params* p, const sol_norm_rope* nr, const void* q, const void* k,
                                 const void* dqo, const void* dko, void* dq, void* dk, float* dq_weight,

@@ -515,3 +515,225 @@ def test_captured_step_replays_on_new_inputs_and_streams(sol):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want2, result(s)))
     sol.sol_last_device_status()
+
+
+# ---- calls that the documentation allows and that are easy to get wrong ------------------------------
+def listed(sol, lists, N, H=1, D=128, seed=4):
+    """A forward pass under routing 1 with lists of the caller's own (the same for every head)."""
+    q, k, v, do = inputs(1, N, H, D, seed)
+    p = sol.make_params(1, N, H, D, topk_ratio=max(0.3, 1.05 * max(map(len, lists)) / len(lists)))
+    buf = sol.alloc_buffers(p, q.device, with_lse=True)
+    sol.sol_pool(p, q, k, v, buf.ws)
+    buf.row_ptr.copy_(torch.tensor(np.cumsum([0] + [len(x) for x in lists] * H), dtype=torch.int32))
+    flat = torch.tensor(sum(lists, []) * H, dtype=torch.int32, device="cuda")
+    buf.col_idx[:len(flat)] = flat
+    sol.sol_attn_fwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
+    return p, buf, [q, k, v, do]
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "do", "lse"])
+def test_non_finite_values_go_where_the_formula_takes_them(sol, where):
+    """One row of NaN: the rows that the lists tie to it get NaN, every other row keeps its bits, the other
+    half of its 128-row tile among them."""
+    lists = [[0, 2], [1, 2, 4], [3], [0, 1, 4], [2], [0, 3], [5, 6], [5], [7]]
+    N, at = 64 * 8 + 30, 64 * 2 + 17
+    p, buf, x = listed(sol, lists, N)
+    g = sol.alloc_grads(p, "cuda")
+    sol.backward(p, *x[:3], buf, x[3], g)
+    clean = [t.clone() for t in (g.dq, g.dk, g.dv)]
+    if where == "lse":
+        buf.lse[..., at] = float("nan")
+    else:
+        x["q k v do".split().index(where)][:, at] = float("nan")
+    sol.backward(p, *x[:3], buf, x[3], g)
+    sol.sol_last_device_status()
+    sel = np.zeros((9, 9), bool)
+    for i, js in enumerate(lists):
+        sel[i, js] = True
+    row, block = np.zeros(N, bool), np.arange(N) // 64
+    row[at] = True
+    asks, asked = sel[:, 2][block], sel[2][block]   # rows whose block lists this one; rows of the blocks that it lists
+    none = np.zeros(N, bool)
+    want = dict(q=(row, asked, asked), k=(asks, row, row), v=(asks, row, none), do=(row, asked, asked),
+                lse=(row, asked, asked))[where]
+    for name, t, c, bad in zip(("dq", "dk", "dv"), (g.dq, g.dk, g.dv), clean, want):
+        bad = torch.from_numpy(bad).cuda()
+        assert torch.isnan(t[0, bad]).all(), name
+        assert torch.equal(t[0, ~bad], c[0, ~bad]), name
+
+
+def test_the_longest_call(sol):
+    """N = 65,536 (1,024 blocks, every word of the bitmaps): blocks at both ends and between, each against
+    the formulas on the rows that its lists tie it to."""
+    N, D = 65536, 64
+    rng = np.random.default_rng(5)
+    lists = [sorted(set(rng.integers(0, 1024, 5).tolist()) | {1023 - i, (7 * i) % 1024}) for i in range(1024)]
+    p, buf, x = listed(sol, lists, N, D=D)
+    g = sol.alloc_grads(p, "cuda")
+    for t in (g.dq, g.dk, g.dv, g.ws):
+        t.fill_(255 if t.dtype == torch.uint8 else float("nan"))
+    sol.backward(p, *x[:3], buf, x[3], g)
+    sol.sol_last_device_status()
+    assert all(torch.isfinite(t).all() for t in (g.dq, g.dk, g.dv))
+    host = [f64(t[0, :, 0]) for t in (*x, buf.o)]
+    lse = f64(buf.lse[0, 0])
+
+    def part(blocks, sel):
+        rows = np.concatenate([np.arange(64 * i, 64 * i + 64) for i in blocks])
+        nb = len(blocks)
+        return rows, train_ref.attention_backward(*(t[rows] for t in host), lse[rows], sel, np.zeros((nb, D)),
+                                                  np.zeros((nb, D)), np.zeros(nb), centroids=False)
+
+    for b in (0, 1, 31, 32, 511, 512, 1022, 1023):
+        for grads, blocks in (((g.dq,), sorted({b, *lists[b]})),
+                              ((g.dk, g.dv), sorted({b, *(i for i in range(1024) if b in lists[i])}))):
+            sel = np.zeros((len(blocks), len(blocks)), bool)
+            me = blocks.index(b)
+            for i, blk in enumerate(blocks):
+                if len(grads) == 1:
+                    sel[me, i] = blk in lists[b]
+                else:
+                    sel[i, me] = b in lists[blk]
+            rows, want = part(blocks, sel)
+            mine = rows // 64 == b
+            for t, (e, bound) in zip(grads, want[:1] if len(grads) == 1 else want[1:]):
+                assert (np.abs(f64(t[0, rows[mine], 0]) - e[mine]) <= bound[mine]).all(), (b, len(grads))
+
+
+def test_the_longest_call_with_centroids(sol):
+    """N = 65,536 without any listed block: 1,024 centroid terms a row, the pooled gradients of all rows."""
+    N, D = 65536, 64
+    p, buf, (q, k, v, do), g = run(sol, 1, N, 1, D, seed=6, tau=50.0)
+    assert int(buf.row_ptr[-1]) == 0
+    w = sol.workspace_views(p, buf.ws)
+    Q, dO, O = (t[0, :, 0].double() for t in (q, do, buf.o))
+    kc, vc, off = (w[n][0, 0].double() for n in ("kbar16", "vbar16", "cbias"))
+    s, U2 = D ** -0.5, 2.0 ** -24
+    prob = torch.exp(s * Q @ kc.T + off - buf.lse[0, 0].double()[:, None])
+    delta, mag = (dO * O).sum(1, True), (dO.abs() * O.abs()).sum(1, True)
+    ds, dsm = prob * (dO @ vc.T - delta), prob * (dO.abs() @ vc.abs().T + mag)
+    e1 = D * float((s * Q.abs() @ kc.abs().T).max()) * U2 + 2.0 ** -20
+    e2 = 2 * D * U2
+
+    def near(got, A, Am, Y, n=1):   # as train_ref.attention_backward bounds a sum of rounded terms
+        want, bound = A @ Y / n, ((U + 2 * e1) * (A.abs() @ Y.abs()) + e2 * (Am @ Y.abs())) / n
+        return ((got - want).abs() <= bound + U * want.abs() + 1e-30).all()
+
+    assert near(g.dq[0, :, 0].double(), s * ds, s * dsm, kc)
+    for t, A, Am, Y in ((g.dk, s * ds.T, s * dsm.T, Q), (g.dv, prob.T, 0 * prob.T, dO)):
+        rows = t[0, :, 0].view(1024, 64, D)
+        assert (rows == rows[:, :1]).all()   # a block's mean: one gradient for its rows
+        assert near(rows[:, 0].double(), A, Am, Y, 64)
+
+
+def test_many_short_sequences(sol):
+    """40,000 sequences of 3 rows, 2 heads: each as in a call of its own."""
+    B, N, H, D = 40000, 3, 2, 64
+    kw = dict(tau=0.5, log_mass_bias=2)
+    q, k, v, do = inputs(B, N, H, D, 12)
+
+    def grads(at):
+        x = [t[at].contiguous() for t in (q, k, v, do)]
+        p = sol.make_params(len(x[0]), N, H, D, **kw)
+        buf = sol.alloc_buffers(p, "cuda", with_lse=True)
+        sol.sol_pool(p, *x[:3], buf.ws)
+        # sol_route takes up to 65,535 heads in all: lists of the caller's, the first head's block exact,
+        # the second's by its centroid
+        buf.row_ptr.copy_((torch.arange(len(buf.row_ptr)) + 1) // 2)
+        buf.col_idx.zero_()
+        sol.sol_attn_fwd(p, *x[:3], buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
+        g = sol.backward(p, *x[:3], buf, x[3], sol.alloc_grads(p, "cuda"))
+        sol.sol_last_device_status()
+        return torch.stack((g.dq, g.dk, g.dv))
+
+    every = grads(slice(None))
+    assert torch.isfinite(every).all() and (every[2] != 0).any(-1).all()
+    for at in (slice(0, 3), slice(21844, 21850), slice(39999, 40000)):
+        assert torch.equal(every[:, at], grads(at))
+
+
+def test_calls_at_once_on_two_streams(sol):
+    """Calls that overlap, each with buffers of its own, give the bits of calls made alone."""
+    N, H, D = 2500, 4, 128
+    p = sol.make_params(1, N, H, D, tau=0.7, log_mass_bias=2, prefix_len=70)
+    sets = []
+    for seed in range(2):
+        q, k, v, do = inputs(1, N, H, D, seed)
+        buf = sol.alloc_buffers(p, "cuda", with_lse=True)
+        sol.forward(p, q, k, v, buf)
+        g = sol.backward(p, q, k, v, buf, do, sol.alloc_grads(p, "cuda"))
+        sets.append((q, k, v, buf, do, g, [t.clone() for t in (g.dq, g.dk, g.dv)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, k, v, buf, do, g, _, s in sets:
+            g.dq.zero_(), g.dk.zero_(), g.dv.zero_()
+        torch.cuda.synchronize()
+        for q, k, v, buf, do, g, _, s in sets:
+            for _ in range(3):
+                sol.backward(p, q, k, v, buf, do, g, stream=s)
+        torch.cuda.synchronize()
+        for *_, g, want, s in sets:
+            assert all(torch.equal(a, b) for a, b in zip((g.dq, g.dk, g.dv), want))
+    sol.sol_last_device_status()
+
+
+def test_captured_autograd_step_beside_an_eager_graph(sol):
+    """Forward and backward captured with leaves of the capture's own, while an eager graph of the same
+    tensors is alive and is run afterwards."""
+    B, N, H, D = 1, 300, 2, 64
+    q, k, w, cos, sin, do, _ = rope_inputs(B, N, H, D, 64, torch.float32, 0, 7)
+    qkv = torch.stack((q, k, torch.randn_like(q)), 2).requires_grad_()
+    w = [t.requires_grad_() for t in w]
+
+    def step(x, wq, wk):
+        a, b, c = x.unbind(2)
+        a, b = sol.qk_norm_rope(a, b, wq, wk, cos, sin)
+        return sol.differentiable_attention(a, b, c.contiguous(), tau=0.4, log_mass_bias=1)
+
+    o = step(qkv, *w)
+    want = torch.autograd.grad(o, (qkv, *w), do, retain_graph=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        leaves = [t.detach().requires_grad_() for t in (qkv, *w)]
+        got = torch.autograd.grad(step(*leaves), leaves, do)
+    graph.replay()
+    o.backward(do)
+    torch.cuda.synchronize()
+    for a, b, c in zip(want, got, (qkv, *w)):
+        assert torch.equal(a, b) and torch.equal(a, c.grad)
+
+
+def test_reblocked_temporaries_belong_to_the_call_s_stream(sol, monkeypatch):
+    """The rows gathered for a call on another stream are not handed out again on the current one while
+    that call may still run."""
+    w = synth.tiny()
+    q, k, v = (parity.to_dev(x) for x in synth.generate(w))
+    p = sol.make_params(w.B, w.N, w.H, w.D, tau=w.tau)
+    rb = sol.alloc_reblock(p, "cuda", with_lse=True)
+    sol.forward_reblocked(p, q, k, v, torch.empty_like(q), rb)
+    g = sol.alloc_grads(p, "cuda")
+    want = [t.clone() for t in (sol.backward_reblocked(p, rb, q, g).dq, g.dk, g.dv)]
+    torch.cuda.synchronize()
+    used = []
+    gather, scatter = sol.sol_gather_rows, sol.sol_scatter_rows
+    monkeypatch.setattr(sol, "sol_gather_rows", lambda p, i, x, y, s=None: (used.append(y.data_ptr()), gather(p, i, x, y, s)))
+    monkeypatch.setattr(sol, "sol_scatter_rows", lambda p, i, x, y, s=None: (used.append(x.data_ptr()), scatter(p, i, x, y, s)))
+    sol.backward_reblocked(p, rb, q, g, stream=torch.cuda.Stream())
+    mine = [torch.empty_like(rb.qp) for _ in range(8)]
+    assert len(used) == 4 and not set(used) & {t.data_ptr() for t in mine}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (g.dq, g.dk, g.dv)))
+
+
+def test_empty_norm_has_zero_weight_gradients(sol):
+    p = sol.make_params(2, 0, 4, 128)
+    dw = [torch.full((128,), float("nan"), device="cuda") for _ in range(2)]
+    x = torch.empty(2, 0, 4, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(1, dtype=torch.uint8, device="cuda")
+    sol.sol_qk_norm_rope_bwd(p, sol.make_norm_rope(None, None), x, x, x, x, x, x, *dw, ws)
+    assert all((t == 0).all() for t in dw)
+    x = x.requires_grad_()
+    w = torch.ones(128, device="cuda", requires_grad=True)
+    sum(t.sum() for t in sol.qk_norm_rope(x, x, w, w)).backward()
+    assert (w.grad == 0).all() and x.grad.shape == x.shape

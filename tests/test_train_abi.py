@@ -166,3 +166,28 @@ def test_no_gpu_is_an_error(sol):
     p = sol.make_params(1, 100, 4, 128)
     assert _bwd(sol, p) == sol.SOL_ERR_CUDA
     assert _fwd_nr(sol, p, _nr(sol)) == sol.SOL_ERR_CUDA
+
+
+def test_tables_and_weights_must_cover_the_call(sol):
+    w, t = torch.ones(64), torch.zeros(10, 32)
+    x = torch.zeros(2, 10, 1, 64, dtype=torch.bfloat16)
+    call = lambda p, nr: sol.sol_qk_norm_rope(p, nr, x, x, x, x)
+    back = lambda p, nr: sol.sol_qk_norm_rope_bwd(p, nr, x, x, x, x, x, x, None, None, x)
+    for p, nr in ((sol.make_params(2, 11, 1, 64), sol.make_norm_rope(w, w, t, t)),                 # a position too many
+                  (sol.make_params(2, 10, 1, 128), sol.make_norm_rope(w, w)),                      # longer heads
+                  (sol.make_params(3, 10, 1, 64), sol.make_norm_rope(w, w, t.expand(2, 10, 32), t.expand(2, 10, 32)))):
+        for f in (call, back):
+            with pytest.raises(ValueError, match="cover"):
+                f(p, nr)
+    with pytest.raises(ValueError):
+        sol.make_norm_rope(torch.ones(64), torch.ones(128))
+    with pytest.raises(ValueError):
+        sol.make_norm_rope(torch.ones(1, 64), None)
+    with pytest.raises(ValueError, match="gradient"):
+        sol.qk_norm_rope(x, x, w, w, t.requires_grad_(), t.detach())
+
+
+def test_empty_call_without_weight_gradients_enqueues_nothing(sol):
+    p = sol.make_params(1, 0, 4, 128)
+    over = dict.fromkeys(("q", "k", "dqo", "dko", "dq", "dk", "dqw", "dkw", "ws"))
+    assert _bwd_nr(sol, p, _nr(sol), **over) == sol.SOL_OK
