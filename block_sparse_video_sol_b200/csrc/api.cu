@@ -423,7 +423,7 @@ namespace {
 
 struct BwdLayout {
   int splits;
-  size_t nlse, ndelta, plan, tplan, gk, gv, gb, coef, da_part, da, counter, total;
+  size_t stat, plan, tplan, gk, gv, gb, coef, da_part, da, counter, total;
 };
 BwdLayout bwd_layout(const sol_params& p) {
   BwdLayout R{};
@@ -432,8 +432,7 @@ BwdLayout bwd_layout(const sol_params& p) {
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   R.splits = attn_bwd_splits((int)nb);
-  R.nlse = take(bh * nb * kBlock * 4);
-  R.ndelta = take(bh * nb * kBlock * 4);
+  R.stat = take(2 * bh * nb * kBlock * 4);
   R.plan = take(tiles * plan_ints(mw, (int)nb) * 4);
   R.tplan = take(tiles * tplan_ints((int)nb) * 4);
   const size_t cent = p.routing == 1 ? 0 : 1, pooled = cent && p.log_mass_bias ? 1 : 0;
@@ -550,7 +549,7 @@ sol_status sol_attn_bwd(const sol_params* p, const void* q, const void* k, const
   a.prefix = p->prefix_len; a.mode = p->log_mass_bias; a.centroids = p->routing == 1 ? 0 : 1;
   a.scale = eff_scale(p);
   a.splits = R.splits;
-  a.nlse = at<float>(bws, R.nlse); a.ndelta = at<float>(bws, R.ndelta);
+  a.stat = at<float>(bws, R.stat);
   a.plan = at<int>(bws, R.plan); a.tplan = at<int>(bws, R.tplan);
   a.gk = at<float>(bws, R.gk); a.gv = at<float>(bws, R.gv); a.gb_ = at<float>(bws, R.gb);
   a.coef = at<float>(bws, R.coef); a.da_part = at<float>(bws, R.da_part);

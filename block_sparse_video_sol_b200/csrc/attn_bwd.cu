@@ -79,14 +79,14 @@ __global__ void __launch_bounds__(256) stat_kernel(const BwdArgs a) {
   __syncthreads();
   for (int e = threadIdx.x; e < kStatRows * heads; e += 256) {
     const int hh = e / kStatRows, r = e % kStatRows, n = n0 + r, h = h0 + hh;
-    const int64_t bh = (int64_t)b * a.H + h, at = bh * 64 * a.nb + n;
+    const int64_t bh = (int64_t)b * a.H + h, at = (bh * a.nb + (n >> 6)) * 128 + (n & 63);
     float nl = -INFINITY, nd = 0.f;
     if (n < a.N) {
       const float l = a.lse[bh * a.N + n];
       if (l != -INFINITY) { nl = -l * kLog2e; nd = -sd[hh][r]; }   // a row without keys: p = 0 everywhere; NaN stays NaN
     }
-    a.nlse[at] = nl;
-    a.ndelta[at] = nd;
+    a.stat[at] = nl;
+    a.stat[at + 64] = nd;
   }
 }
 
@@ -230,6 +230,7 @@ struct Cfg {
 // buffers filled by the planning warp while the previous tile runs.
 struct DqTile {
   int tile, n_union, n_cent;                      // tile < 0: no more
+  int i0, bh, h, b;                               // its first query block and head
   int list[kMaxKeyBlocks];                        // union entries: j | needA << 16 | needB << 17
   int clist[16];                                  // 64-centroid units: u | liveA << 16 | liveB << 17
   alignas(16) float cent_add[16][2][64];          // their offsets (log2 units), -inf where masked
@@ -257,9 +258,10 @@ struct DqExtra {
 
 struct KvTile {
   int tile, n;                                    // tile < 0: no more
+  int tk, bh, h, b, split;                        // its index in the head, its head, its query range (centroids)
   int list[kMaxKeyBlocks];                        // query blocks: i | needA << 16 | needB << 17
   uint32_t cword[128][4];                         // centroids: each step's exact-block bits of the tile
-  alignas(16) float gsum[2][2][128];              // exact: the two blocks' gk, gv
+  alignas(16) float gsum[4 * 128];                // exact: [gk, gv][block][D] of the tile's two blocks
   float coef[3][128];                             // and the rows' alpha, beta, gamma
 };
 struct KvBars {
@@ -270,26 +272,34 @@ struct KvBars {
   uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
   uint64_t p_full[2], ds_full[2];   // P is in S's place / dS is in dP's place
   uint64_t acc_full[2], acc_clear[2];   // dK / dV are complete; read and zeroed for the next tile
-  uint64_t gb_full, out_full;       // group 0's offset sums are there; the results are in their ring slots, to be stored
+  uint64_t gb_full, out_full[2];    // group 0's offset sums are there; dK / dV are in their ring slots, to be stored
   uint64_t mma_done;                // the issuers' last commits, at the end
 };
 struct KvExtra {
   KvBars bar;
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float nl[4][64], nd[4][64];         // per ring slot: -lse, -delta of the query rows
+  alignas(16) float stat[4][128];                 // per ring slot: -lse and -delta of the query rows
   float gb[2][128];
   KvTile info[2];
 };
 
-// TMA loads of one streamed pair (two 64-row tiles).
-template <int D>
-__device__ __forceinline__ void load_pair4(uint8_t* dst, const CUtensorMap* m1, const CUtensorMap* m2, int row, int h, int b,
-                                           uint64_t* bar) {
-  for (int c = 0; c < Cfg<D>::kChunks; ++c) {
-    tma_load_4d(dst + c * Cfg<D>::kSChunk, m1, c * 64, h, row, b, bar);
-    tma_load_4d(dst + Cfg<D>::kSTile + c * Cfg<D>::kSChunk, m2, c * 64, h, row, b, bar);
-  }
+// TMA load of a tile of a BTHD tensor: one instruction, since one takes its thread some
+// 150 clocks and steps are short.  The maps have the 64-column chunks as a dimension
+// of their own outside the rows, which is the tiles' layout.
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* m, int row, int h, int b, uint64_t* bar) {
+  tma_load_5d(dst, m, 0, row, 0, h, b, bar);
+}
+
+// A plan's list (up to nb entries) into shared memory by one warp; returns its length.  The
+// length and the first 64 entries are read at once: a tile of few steps waits for this.
+__device__ __forceinline__ int copy_list(int* dst, const int* src, const int* length, int nb, int lane) {
+  const int a = lane < nb ? src[lane] : 0, b = 32 + lane < nb ? src[32 + lane] : 0, n = *length;
+  dst[lane] = a;
+  dst[32 + lane] = b;
+#pragma unroll 4
+  for (int e = 64 + lane; e < n; e += 32) dst[e] = src[e];
+  return n;
 }
 
 // Rows of half hf that a step with this list entry leaves out of its MMAs.
@@ -339,14 +349,10 @@ __device__ __forceinline__ void put_row(uint8_t* tile, int r, int c, const float
                    pack_bf16(v[8 * u + 4], v[8 * u + 5]), pack_bf16(v[8 * u + 6], v[8 * u + 7]));
   }
 }
-// The same tile's halves to rows row0 .. row0 + 127 of a BTHD tensor (one thread).
-template <int D>
-__device__ __forceinline__ void store_rows(const CUtensorMap* m, const uint8_t* tile, int row0, int h, int b, int N) {
-  for (int hf = 0; hf < 2; ++hf)
-    if (row0 + 64 * hf < N)
-      for (int c = 0; c < Cfg<D>::kChunks; ++c)
-        tma_store_4d(m, c * 64, h, row0 + 64 * hf, b, tile + c * Cfg<D>::kOChunk + hf * (Cfg<D>::kOChunk / 2));
-  tma_store_wait();
+// The same tile to rows row0 .. row0 + 127 of a BTHD tensor (one thread; rows past N are not written).
+__device__ __forceinline__ void store_rows(const CUtensorMap* m, const uint8_t* tile, int row0, int h, int b) {
+  tma_store_5d(m, 0, row0, 0, h, b, tile);
+  tma_store_commit();
 }
 
 // The queries' pass is persistent: a CTA takes tiles off a counter until none is
@@ -416,14 +422,10 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
         if (!(ok = ok && wait(&bar.plan_full[k & 1], k >> 1))) break;
         const DqTile& in = x.info[k & 1];
         if (in.tile < 0) break;
-        const int64_t bh = in.tile / ntq;
-        const int i0 = 2 * (in.tile % ntq), h = (int)(bh % a.H), b = (int)(bh / a.H), T = in.steps();
+        const int h = in.h, b = in.b, T = in.steps();
         for (int o = 0; o < 2 && slot(); ++o, next()) {   // Q, dO
           mbar_expect_tx(&bar.full[pos.s], C::kOTile);
-          for (int c = 0; c < C::kChunks; ++c)
-            for (int hf = 0; hf < 2; ++hf)
-              tma_load_4d(ring + pos.s * C::kOTile + c * C::kOChunk + hf * (C::kOChunk / 2), o ? &mdo : &mq, c * 64, h, 64 * (i0 + hf), b,
-                          &bar.full[pos.s]);
+          load_rows(ring + pos.s * C::kOTile, o ? &mdo : &mq, 64 * in.i0, h, b, &bar.full[pos.s]);
         }
         const int go = max(0, T - kAhead);
         if (T == 0) mbar_arrive(&bar.plan_go);
@@ -434,12 +436,11 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
           mbar_expect_tx(full, 2 * C::kSTile);
           const int row = 64 * (in.entry(t) & 0xffff);
           if (t < in.n_union) {
-            load_pair4<D>(dst, &mk, &mv, row, h, b, full);
+            load_rows(dst, &mk, row, h, b, full);
+            load_rows(dst + C::kSTile, &mv, row, h, b, full);
           } else {
-            for (int c = 0; c < C::kChunks; ++c) {
-              tma_load_3d(dst + c * C::kSChunk, &mkb, c * 64, row, (int)bh, full);
-              tma_load_3d(dst + C::kSTile + c * C::kSChunk, &mvb, c * 64, row, (int)bh, full);
-            }
+            tma_load_4d(dst, &mkb, 0, row, 0, in.bh, full);
+            tma_load_4d(dst + C::kSTile, &mvb, 0, row, 0, in.bh, full);
           }
         }
         if (!slot()) break;   // the slot that carries dQ out: handed over empty
@@ -568,26 +569,30 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
       }
       tile = tile_at(tile, a.B * a.H, ntq, min(ntq, (a.prefix + 127) / 128));
       const int* P = a.plan + (int64_t)tile * plan_ints(mw, a.nb);
-      const int n = P[0];
+      const int n = copy_list(in.list, P + 16 + 2 * mw, P, a.nb, lane);
       const uint32_t w0 = (uint32_t)P[12], w1 = (uint32_t)P[13];   // bitmap words that leave a block to its centroid
       const bool l0 = lane < 16 && ((w0 >> (2 * lane)) & 3u), l1 = lane < 16 && ((w1 >> (2 * lane)) & 3u);
       const uint32_t any = __ballot_sync(0xffffffffu, l0 || l1);
       if (l0 || l1) in.clist[__popc(any & ((1u << lane) - 1u))] = lane | (int)l0 << 16 | (int)l1 << 17;
-#pragma unroll 4
-      for (int e = lane; e < n; e += 32) in.list[e] = P[16 + 2 * mw + e];
-      if (lane == 0) { in.tile = tile; in.n_union = n; in.n_cent = __popc(any); }
+      const int bh = tile / ntq, i0 = 2 * (tile % ntq), nc = __popc(any);
+      if (lane == 0) {
+        in.tile = tile; in.n_union = n; in.n_cent = nc;
+        in.i0 = i0; in.bh = bh; in.h = bh % a.H; in.b = bh / a.H;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.plan_full[k & 1]);
-      const int64_t bh = tile / ntq;
-      const int i0 = 2 * (tile % ntq), nc = __popc(any);
       for (int s = 0; s < nc; ++s) {
         const int unit = in.clist[s] & 0xffff;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int e = lane + 32 * q, hf = e >> 6, j = 64 * unit + (e & 63);
-          float v = -INFINITY;
-          if (j < a.nb && i0 + hf < a.nb && !(((uint32_t)P[16 + hf * mw + (j >> 5)] >> (j & 31)) & 1u)) v = a.cbias[bh * a.nb + j] * kLog2e;
-          in.cent_add[s][hf][e & 63] = v;
+          uint32_t bits = 0xffffffffu;   // (both loads at once)
+          float v = 0.f;
+          if (j < a.nb && i0 + hf < a.nb) {
+            bits = (uint32_t)P[16 + hf * mw + (j >> 5)];
+            v = a.cbias[(int64_t)bh * a.nb + j] * kLog2e;
+          }
+          in.cent_add[s][hf][e & 63] = (bits >> (j & 31)) & 1u ? -INFINITY : v;
         }
       }
       __syncwarp();
@@ -603,7 +608,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
       pos.skip(2 + in.steps());
       if (!wait_w(&bar.out_full, k)) break;
       if (lane == 0) {
-        store_rows<D>(&mdq, ring + pos.s * C::kOTile, 128 * (in.tile % ntq), (in.tile / ntq) % a.H, in.tile / ntq / a.H, a.N);
+        store_rows(&mdq, ring + pos.s * C::kOTile, 64 * in.i0, in.h, in.b);
+        tma_store_wait<0>();
         mbar_arrive(&bar.empty[pos.s]);
       }
       pos.next();
@@ -620,10 +626,10 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     float nl = 0.f, nd = 0.f;
     // A tile's rows: -lse and -delta, and Q (group 0) or dO (group 1) from its slot into TMEM
     auto take_own = [&](const DqTile& in) {
-      const int i = 2 * (in.tile % ntq) + hf;
-      const int64_t at = (int64_t)(in.tile / ntq) * 64 * a.nb + 64 * i + (r & 63);
-      nl = i < a.nb ? a.nlse[at] : -INFINITY;
-      nd = i < a.nb ? a.ndelta[at] : 0.f;
+      const int i = in.i0 + hf;
+      const float* st = a.stat + ((int64_t)in.bh * a.nb + i) * 128 + (r & 63);
+      nl = i < a.nb ? st[0] : -INFINITY;
+      nd = i < a.nb ? st[64] : 0.f;
       RingPos<S> p = pos;
       if (g) p.next();
       if (!wait_w(&bar.full[p.s], p.ph)) return false;
@@ -663,7 +669,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
     for (int k = 0; ok; ++k) {
       const DqTile& in = x.info[k & 1];
       if (in.tile < 0) break;
-      const int n_union = in.n_union, T = in.steps(), tile = in.tile;
+      const int n_union = in.n_union, T = in.steps();
       const uint64_t nl2 = f2pack(nl, nl), nd2 = f2pack(nd, nd);
       for (int u = base + ((base + g) & 1); u < base + T; u += 2) {   // the steps of this group's stage
         const int t = u - base, e = in.entry(t);
@@ -742,10 +748,10 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
       // dQ into its slot, from where the planning warp stores it
       if (!(ok = wait_w(&bar.dq_full, k) && wait_w(&bar.full[out.s], out.ph))) break;
       fence_after();
-      const int row = 128 * (tile % ntq) + r;
+      const int row = 64 * in.i0 + r;
       const bool anch = a.da && (row >= a.prefix || a.prefix == a.N);
       if (a.da && k == 0) griddep_wait();   // launched early: the anchor's gradient has to be there from here on
-      const float4* da = reinterpret_cast<const float4*>(a.da + (int64_t)(tile / ntq) * D);
+      const float4* da = reinterpret_cast<const float4*>(a.da + (int64_t)in.bh * D);
 #pragma unroll 1
       for (int c = g; c < D / 16; c += 2) {
         float v[16];
@@ -803,7 +809,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntq = (a.nb + 1) / 2, mw = a.mask_words;
   const int tiles = kCent ? (a.nb + 127) / 128 : ntq;   // of one head (and range)
-  const int64_t bhs = (int64_t)a.B * a.H;
+  const int bhs = a.B * a.H;
 
   if (kCent) griddep_wait();   // the plans and row statistics: the passes after this one rely on them without a wait
   griddep_launch();            // the next pass may take up idle SMs
@@ -817,7 +823,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     }
     for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
     mbar_init(&bar.gb_full, 128);
-    mbar_init(&bar.out_full, 8);
+    for (int s = 0; s < 2; ++s) mbar_init(&bar.out_full[s], 4);
     mbar_init(&bar.plan_go, 1);
     mbar_init(&bar.mma_done, 2);
     x.abort_flag = 0;
@@ -846,18 +852,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         if (!(ok = ok && wait(&bar.plan_full[k & 1], k >> 1))) break;
         const KvTile& in = x.info[k & 1];
         if (in.tile < 0) break;
-        const int tk = in.tile % tiles;
-        const int64_t bh = (in.tile / tiles) % bhs;
-        const int h = (int)(bh % a.H), b = (int)(bh / a.H), T = in.n;
+        const int tk = in.tk, h = in.h, b = in.b, T = in.n;
         for (int o = 0; o < 2; ++o) {   // K, V, once the previous tile's products have read theirs
           if (k > 0 && !(ok = ok && wait(&bar.own_free[o], k - 1))) break;
           mbar_expect_tx(&bar.own_full[o], C::kOTile);
-          for (int c = 0; c < C::kChunks; ++c)
-            for (int hf = 0; hf < 2; ++hf) {
-              uint8_t* dst = own + o * C::kOTile + c * C::kOChunk + hf * (C::kOChunk / 2);
-              if (kCent) tma_load_3d(dst, o ? &mv : &mk, c * 64, 128 * tk + 64 * hf, (int)bh, &bar.own_full[o]);
-              else tma_load_4d(dst, o ? &mv : &mk, c * 64, h, 128 * tk + 64 * hf, b, &bar.own_full[o]);
-            }
+          if (kCent) tma_load_4d(own + o * C::kOTile, o ? &mv : &mk, 0, 128 * tk, 0, in.bh, &bar.own_full[o]);
+          else load_rows(own + o * C::kOTile, o ? &mv : &mk, 128 * tk, h, b, &bar.own_full[o]);
         }
         if (!ok) break;
         ++owns;
@@ -867,9 +867,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
           if (t == go) mbar_arrive(&bar.plan_go);
           const int i = in.list[t] & 0xffff;
           mbar_expect_tx(&bar.full[pos.s], 2 * C::kSTile + 512);
-          load_pair4<D>(ring + pos.s * C::kOTile, &mq, &mdo, 64 * i, h, b, &bar.full[pos.s]);
-          bulk_load(x.nl[pos.s], a.nlse + (bh * a.nb + i) * 64, 256, &bar.full[pos.s]);
-          bulk_load(x.nd[pos.s], a.ndelta + (bh * a.nb + i) * 64, 256, &bar.full[pos.s]);
+          load_rows(ring + pos.s * C::kOTile, &mq, 64 * i, h, b, &bar.full[pos.s]);
+          load_rows(ring + pos.s * C::kOTile + C::kSTile, &mdo, 64 * i, h, b, &bar.full[pos.s]);
+          bulk_load(x.stat[pos.s], a.stat + ((int64_t)in.bh * a.nb + i) * 128, 512, &bar.full[pos.s]);
         }
         for (int o = 0; o < kOut && slot(); ++o, next()) mbar_arrive(&bar.full[pos.s]);   // handed over empty
         if (!ok) break;
@@ -929,14 +929,14 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       fence_after();
       int u = base, e0 = T > 0 ? entry(0) : 0, e1 = T > 1 ? entry(1) : 0, e2 = T > 2 ? entry(2) : 0;   // steps u, u+1, u+2
       for (; u < base + T - 2 && ok; ++u) {   // (no condition around a batch: see the last two steps below)
-        ok = wait_ld() && wait(&ready[u & 1], u >> 1);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (!(ok = wait_w(&ready[u & 1], u >> 1))) break;
         fence_after();
         finish(u & 1, e0);
         const int e = e2;
         e0 = e1;
         e1 = e2;
         e2 = entry(min(u + 3 - base, T - 1));
+        if (!(ok = __all_sync(0xffffffffu, wait_ld()))) break;
         start(u & 1, e);
       }
       mma_commit_w(&bar.own_free[o]);
@@ -957,7 +957,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     if (first) drain_bar(&bar.mma_done, 0, a.status);
   } else if (warp == 3) {
     // ---------------------------------------------------------------- plans, and the results' way out
-    const int64_t total = bhs * tiles * (kCent ? a.splits : 1);
+    const int total = bhs * tiles * (kCent ? a.splits : 1);
     auto plan = [&](int k) {   // the next tile off the counter into buffer k & 1
       KvTile& in = x.info[k & 1];
       int tile = 0;
@@ -968,16 +968,14 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         return;
       }
       if (!kCent) tile = tile_at(tile, a.B * a.H, tiles, min(tiles, (a.prefix + 127) / 128));
-      const int tk = tile % tiles;
-      const int64_t bh = (tile / tiles) % bhs;
+      const int tk = tile % tiles, at = tile / tiles, bh = kCent ? at % bhs : at, split = kCent ? at / bhs : 0;
       int n = 0;
       if (kCent) {   // the range's query blocks that leave any of the tile's key blocks to its centroid
-        const int split = (int)(tile / tiles / bhs);
         const int lo = (int)((int64_t)a.nb * split / a.splits), hi = (int)((int64_t)a.nb * (split + 1) / a.splits);
         for (int i = lo; i < hi; i += 32) {
           uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
           if (i + lane < hi) {
-            const int* P = a.plan + (bh * ntq + ((i + lane) >> 1)) * plan_ints(mw, a.nb) + 16 + ((i + lane) & 1) * mw;
+            const int* P = a.plan + ((int64_t)bh * ntq + ((i + lane) >> 1)) * plan_ints(mw, a.nb) + 16 + ((i + lane) & 1) * mw;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int first = 128 * tk + 32 * e;
@@ -998,11 +996,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         }
       } else {
         const int* P = a.tplan + (int64_t)tile * tplan_ints(a.nb);
-        n = P[0];
-#pragma unroll 4
-        for (int e = lane; e < n; e += 32) in.list[e] = P[16 + e];
+        n = copy_list(in.list, P + 16, P, a.nb, lane);
       }
-      if (lane == 0) { in.tile = tile; in.n = n; }
+      if (lane == 0) {
+        in.tile = tile; in.n = n;
+        in.tk = tk; in.bh = bh; in.h = bh % a.H; in.b = bh / a.H; in.split = split;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.plan_full[k & 1]);
     };
@@ -1011,32 +1010,48 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     auto plan_cent = [&](int k) {
       KvTile& in = x.info[k & 1];
       if (in.tile < 0) return;
-      const int tk = in.tile % tiles;
-      const int64_t bh = (in.tile / tiles) % bhs;
+      const int tk = in.tk;
+      const int64_t bh = in.bh;
       if (!kCent && k == 0) griddep_wait();   // launched early: the centroids' pass has to be complete from here on
       if (!kCent && a.centroids) {   // the two blocks' centroid gradients, summed over the query ranges in order
-        for (int e = lane; e < D; e += 32) {   // float4s of [gk, gv][half][D]
-          const int d = e % (D / 4), half = (e / (D / 4)) & 1, which = e / (D / 2), jj = 2 * tk + half;
-          const float4* src = reinterpret_cast<const float4*>((which ? a.gv : a.gk) + (bh * a.nb + jj) * D) + d;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (jj < a.nb) {
-#pragma unroll 4
-            for (int s = 0; s < a.splits; ++s) {
-              const float4 q = src[s * bhs * a.nb * (D / 4)];
-              v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+        // (all loads of four ranges in flight together: tiles of few steps wait for this warp)
+        float4 sum[D / 32];   // float4s e = lane + 32 i of [gk, gv][half][D]
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int s0 = 0; s0 < a.splits; s0 += 4) {
+          float4 q[4][D / 32];
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const int e = lane + 32 * i, d = e % (D / 4), jj = 2 * tk + ((e / (D / 4)) & 1);
+              q[s][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (s0 + s < a.splits && jj < a.nb)
+                q[s][i] = reinterpret_cast<const float4*>((e < D / 2 ? a.gk : a.gv) + (((s0 + s) * bhs + bh) * a.nb + jj) * D)[d];
             }
-          }
-          reinterpret_cast<float4*>(in.gsum[which][half])[d] = v;
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              sum[i].x += q[s][i].x; sum[i].y += q[s][i].y; sum[i].z += q[s][i].z; sum[i].w += q[s][i].w;
+            }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {   // the rows' coefficients alpha, beta, gamma
+        for (int i = 0; i < D / 32; ++i) reinterpret_cast<float4*>(in.gsum)[lane + 32 * i] = sum[i];
+        float cf[4][3];   // the rows' coefficients alpha, beta, gamma
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
           const int row = 128 * tk + 32 * q + lane, jj = row >> 6;
-          const int64_t plane = bhs * 64 * a.nb, at = bh * 64 * a.nb + row;
+          const int64_t plane = (int64_t)bhs * 64 * a.nb, at = bh * 64 * a.nb + row;
           const float even = 1.f / (float)min(64, max(1, a.N - 64 * jj));
 #pragma unroll
-          for (int o = 0; o < 3; ++o)
-            in.coef[o][32 * q + lane] = row >= a.N ? 0.f : a.mode ? a.coef[o * plane + at] : o == 1 ? 0.f : even;
+          for (int o = 0; o < 3; ++o) cf[q][o] = row >= a.N ? 0.f : a.mode ? a.coef[o * plane + at] : o == 1 ? 0.f : even;
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int o = 0; o < 3; ++o) in.coef[o][32 * q + lane] = cf[q][o];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.plan_cent[k & 1]);
@@ -1050,28 +1065,31 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (!wait_w(&bar.plan_go, k) || (k >= 1 && !wait_w(&bar.plan_empty[(k + 1) & 1], ((k + 1) >> 1) - 1))) break;
       plan(k + 1);
       pos.skip(in.n);
-      if (!wait_w(&bar.out_full, k)) break;
-      if (lane == 0) {
-        const int tk = in.tile % tiles;
-        const int64_t bh = (in.tile / tiles) % bhs;
-        RingPos<S> q = pos;
-        if (kCent) {
-          const int plane = (int)((in.tile / tiles / bhs) * bhs + bh);
-          for (int o = 0; o < 2; ++o)
+      // dV, then dK, each as it is ready; its slots are free (two arrivals each) once the stores have read them
+      const int row0 = 128 * in.tk, h = in.h, b = in.b, plane = in.split * bhs + in.bh;
+      RingPos<S> q = pos;
+      bool ok = true;
+      for (int o = 1; o >= 0 && (ok = wait_w(&bar.out_full[o], k)); --o) {
+        if (lane == 0) {
+          if (kCent) {
             for (int c = 0; c < D / 32; ++c) {
               const int at = c * C::kOChunk;
               RingPos<S> w = q;
-              w.skip(2 * o + at / C::kOTile);
-              tma_store_3d(o ? &mgv : &mgk, 32 * c, 128 * tk, plane, ring + w.s * C::kOTile + at % C::kOTile);
+              w.skip(at / C::kOTile);
+              tma_store_3d(o ? &mgv : &mgk, 32 * c, row0, plane, ring + w.s * C::kOTile + at % C::kOTile);
             }
-          tma_store_wait();
-        } else {
-          const int h = (int)(bh % a.H), b = (int)(bh / a.H);
-          store_rows<D>(&mgk, ring + q.s * C::kOTile, 128 * tk, h, b, a.N);
-          q.next();
-          store_rows<D>(&mgv, ring + q.s * C::kOTile, 128 * tk, h, b, a.N);
+            tma_store_commit();
+          } else {
+            store_rows(o ? &mgv : &mgk, ring + q.s * C::kOTile, row0, h, b);
+          }
         }
-        for (int o = 0; o < kOut; ++o) {   // (two arrivals free a slot)
+        q.skip(kOut / 2);
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        for (int o = 0; o < kOut; ++o) {
+          if (o == 0) tma_store_wait<1>();
+          if (o == kOut / 2) tma_store_wait<0>();
           RingPos<S> w = pos;
           w.skip(o);
           mbar_arrive(&bar.empty[w.s]);
@@ -1082,6 +1100,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       __syncwarp();
       plan_cent(k + 1);
     }
+    if (lane == 0) tma_store_wait<0>();
   } else {
     // ---------------------------------------------------------------- softmax warpgroups
     const int g = (warp >> 2) - 1, sub = warp & 3, r = 32 * sub + lane, hf = r >> 6;
@@ -1107,8 +1126,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (!(ok = wait_w(&bar.plan_full[k & 1], k >> 1))) break;
       const KvTile& in = x.info[k & 1];
       if (in.tile < 0) break;
-      const int T = in.n, tk = in.tile % tiles;
-      const int64_t bh = (in.tile / tiles) % bhs;
+      const int T = in.n, tk = in.tk;
+      const int64_t bh = in.bh;
       const int j = kCent ? 128 * tk + r : 2 * tk + hf;   // this row's centroid / key block
       const float cadd = kCent && j < a.nb ? a.cbias[bh * a.nb + j] * kLog2e : -INFINITY;
       uint64_t gb2 = 0ull;   // kCent: the sums of ds of even and odd queries
@@ -1136,7 +1155,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float4 l4 = reinterpret_cast<const float4*>(x.nl[rs])[c];
+            const float4 l4 = reinterpret_cast<const float4*>(x.stat[rs])[c];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint64_t l2 = q ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y);
@@ -1165,7 +1184,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float4 d4 = reinterpret_cast<const float4*>(x.nd[rs])[8 * hh + c];
+              const float4 d4 = reinterpret_cast<const float4*>(x.stat[rs] + 64)[8 * hh + c];
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 const uint64_t n2 = q ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y);
@@ -1192,7 +1211,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (!(ok = wait_w(&bar.acc_full[g], k) && wait_w(&bar.plan_cent[k & 1], k >> 1))) break;
       fence_after();
       RingPos<S> out = pos;
-      out.skip(g * (kOut / 2));
+      out.skip((1 - g) * (kOut / 2));   // (dV is done first)
       pos.skip(kOut);
       if (kCent) {
         float gbs, odd;
@@ -1203,8 +1222,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
           mbar_arrive(&bar.gb_full);
         } else {
           if (!(ok = wait_w(&bar.gb_full, k))) break;
-          const int64_t split = in.tile / tiles / bhs;
-          if (j < a.nb) a.gb_[(split * bhs + bh) * a.nb + j] = x.gb[k & 1][r] + gbs;
+          if (j < a.nb) a.gb_[((int64_t)in.split * bhs + bh) * a.nb + j] = x.gb[k & 1][r] + gbs;
         }
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {   // fp32 rows: 32-column chunks of 128 bytes, SW128
@@ -1227,7 +1245,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         // the row's share of its centroid's gradient, and of the anchor's
         const float mul = in.coef[g ? 2 : 0][r], beta = in.coef[1][r];
         const float4* an = reinterpret_cast<const float4*>(a.anchor + bh * D);
-        const float4* gs = reinterpret_cast<const float4*>(in.gsum[g][hf]);
+        const float4* gs = reinterpret_cast<const float4*>(in.gsum + (2 * g + hf) * D);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
@@ -1261,7 +1279,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       fence_before();
       mbar_arrive(&bar.acc_clear[g]);
       __syncwarp();
-      if (lane == 0) { mbar_arrive(&bar.out_full); mbar_arrive(&bar.plan_empty[k & 1]); }
+      if (lane == 0) { mbar_arrive(&bar.out_full[g]); mbar_arrive(&bar.plan_empty[k & 1]); }
     }
   }
   fence_before();
@@ -1438,20 +1456,19 @@ cudaError_t prepare() {
 }
 
 // 64-row boxes of a BTHD tensor (strides in elements) and of the [BH, nb, D] centroids.
-bool map_rows(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D, int64_t sb, int64_t sn, int64_t sh) {
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.N, (cuuint64_t)a.B};
-  const cuuint64_t str[3] = {(cuuint64_t)(a.H > 1 ? sh : D) * 2, (cuuint64_t)(a.N > 1 ? sn : D) * 2,
+bool map_rows(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D, int64_t sb, int64_t sn, int64_t sh, int rows) {
+  const cuuint64_t dims[5] = {64, (cuuint64_t)a.N, (cuuint64_t)D / 64, (cuuint64_t)a.H, (cuuint64_t)a.B};
+  const cuuint64_t str[4] = {(cuuint64_t)(a.N > 1 ? sn : D) * 2, 128, (cuuint64_t)(a.H > 1 ? sh : D) * 2,
                              (cuuint64_t)(a.B > 1 ? sb : D) * 2};
-  const cuuint32_t box[4] = {64, 1, 64, 1};
+  const cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)D / 64, 1, 1};
+  return make_map(m, p, 5, dims, str, box, kSw128);
+}
+bool map_cent(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D, int rows) {
+  const cuuint64_t dims[4] = {64, (cuuint64_t)a.nb, (cuuint64_t)D / 64, (cuuint64_t)a.B * a.H};
+  const cuuint64_t str[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)a.nb * D * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)D / 64, 1};
   return make_map(m, p, 4, dims, str, box, kSw128);
 }
-bool map_cent(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D) {
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.nb, (cuuint64_t)a.B * a.H};
-  const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.nb * D * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
-  return make_map(m, p, 3, dims, str, box, kSw128);
-}
-// 128-row boxes of the centroid gradients' partial sums, fp32 [splits * BH, nb, D].
 bool map_part(CUtensorMap* m, const float* p, const BwdArgs& a, int D) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.nb, (cuuint64_t)a.splits * a.B * a.H};
   const cuuint64_t str[2] = {(cuuint64_t)D * 4, (cuuint64_t)a.nb * D * 4};
@@ -1461,12 +1478,17 @@ bool map_part(CUtensorMap* m, const float* p, const BwdArgs& a, int D) {
 
 template <int D>
 cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mdo, mkb, mvb, mdq, mdk, mdv, mgk, mgv;
-  if (!map_rows(&mq, a.q, a, D, a.sb, a.sn, a.sh) || !map_rows(&mk, a.k, a, D, a.sb, a.sn, a.sh) ||
-      !map_rows(&mv, a.v, a, D, a.sb, a.sn, a.sh) || !map_rows(&mdo, a.d_o, a, D, a.ob, a.on, a.oh) ||
-      !map_cent(&mkb, a.kbar16, a, D) || !map_cent(&mvb, a.vbar16, a, D) || !map_rows(&mdq, a.dq, a, D, a.gb, a.gn, a.gh) ||
-      !map_rows(&mdk, a.dk, a, D, a.gb, a.gn, a.gh) || !map_rows(&mdv, a.dv, a, D, a.gb, a.gn, a.gh) ||
-      (a.centroids && (!map_part(&mgk, a.gk, a, D) || !map_part(&mgv, a.gv, a, D))))
+  // 64-row boxes where a tile is streamed, 128-row ones (`o`) where it is owned or a result
+  CUtensorMap mq, mk, mv, mdo, mkb, mvb, oq, ok, ov, odo, okb, ovb, mdq, mdk, mdv, mgk, mgv;
+  auto in = [&](CUtensorMap* m, CUtensorMap* o, const __nv_bfloat16* p, int64_t sb, int64_t sn, int64_t sh) {
+    return map_rows(m, p, a, D, sb, sn, sh, 64) && map_rows(o, p, a, D, sb, sn, sh, 128);
+  };
+  auto out = [&](CUtensorMap* m, const __nv_bfloat16* p) { return map_rows(m, p, a, D, a.gb, a.gn, a.gh, 128); };
+  if (!in(&mq, &oq, a.q, a.sb, a.sn, a.sh) || !in(&mk, &ok, a.k, a.sb, a.sn, a.sh) || !in(&mv, &ov, a.v, a.sb, a.sn, a.sh) ||
+      !in(&mdo, &odo, a.d_o, a.ob, a.on, a.oh) || !out(&mdq, a.dq) || !out(&mdk, a.dk) || !out(&mdv, a.dv) ||
+      !map_cent(&mkb, a.kbar16, a, D, 64) || !map_cent(&mvb, a.vbar16, a, D, 64) ||
+      (a.centroids && (!map_cent(&okb, a.kbar16, a, D, 128) || !map_cent(&ovb, a.vbar16, a, D, 128) ||
+                       !map_part(&mgk, a.gk, a, D) || !map_part(&mgv, a.gv, a, D))))
     return cudaErrorInvalidValue;
   cudaError_t e = prepare<D>();
   if (e != cudaSuccess) return e;
@@ -1491,16 +1513,16 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   if ((e = launch_kernel(tplan_kernel, dim3(bh, a.mask_words), kTWarps * 32, 0, st, few, a)) != cudaSuccess) return e;
   if (a.centroids) {
     const unsigned n = std::min(bh * ((a.nb + 127) / 128) * a.splits, kSms);
-    e = launch_kernel(dkv_kernel<D, true>, n, kThreads, dkv_smem<D>(), st, true, mq, mdo, mkb, mvb, mgk, mgv, a);
+    e = launch_kernel(dkv_kernel<D, true>, n, kThreads, dkv_smem<D>(), st, true, mq, mdo, okb, ovb, mgk, mgv, a);
     if (e != cudaSuccess) return e;
     if (a.mode) {
       if ((e = launch_kernel(pool_bwd_kernel<D>, dim3(bh, a.nb), 256, 0, st, few, a)) != cudaSuccess) return e;
       if ((e = launch_kernel(anchor_bwd_kernel<D>, bh, 1024, 0, st, true, a)) != cudaSuccess) return e;
     }
   }
-  e = launch_kernel(dq_kernel<D>, std::min(tiles, kSms), kThreads, dq_smem<D>(), st, a.centroids != 0, mq, mdo, mdq, mk, mv, mkb, mvb, a);
+  e = launch_kernel(dq_kernel<D>, std::min(tiles, kSms), kThreads, dq_smem<D>(), st, a.centroids != 0, oq, odo, mdq, mk, mv, mkb, mvb, a);
   if (e != cudaSuccess) return e;
-  return launch_kernel(dkv_kernel<D, false>, std::min(tiles, kSms), kThreads, dkv_smem<D>(), st, true, mq, mdo, mk, mv, mdk, mdv, a);
+  return launch_kernel(dkv_kernel<D, false>, std::min(tiles, kSms), kThreads, dkv_smem<D>(), st, true, mq, mdo, ok, ov, mdk, mdv, a);
 }
 
 }  // namespace

@@ -187,8 +187,8 @@ struct BwdArgs {
   float scale;
   int splits;                    // query ranges of the centroid pass
   // caller-owned workspace
-  float* nlse;                   // [BH][64 nb]  -lse in log2 units, -inf for rows without keys or past N
-  float* ndelta;                 // [BH][64 nb]  -sum_d dO O, 0 past N
+  float* stat;                   // [BH][nb][2][64]: -lse in log2 units (-inf for rows without keys or past N)
+                                 // and -sum_d dO O (0 past N) of a block's rows
   int* plan;                     // [BH * ceil(nb/2)][plan_ints]
   int* tplan;                    // [BH * ceil(nb/2)][tplan_ints]
   float* gk; float* gv;          // [splits][BH][nb][D] centroid gradients (gk scaled by s)
