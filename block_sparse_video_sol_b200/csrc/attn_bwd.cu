@@ -156,22 +156,35 @@ __global__ void __launch_bounds__(kTWarps * 32) tplan_kernel(const BwdArgs a) {
 // lists whose steps mostly concern one half this is what sets the clock of long
 // calls (a loop of such MMAs, 148 SMs at the 1 kW limit: 1.58 GHz unmasked, 1.85
 // GHz with half the rows masked).  Accumulators start from zeros stored by the
-// softmax threads, since a half's first step may not be the tile's.  Roles (12 warps): warp 0 loads the tiles with TMA, warps 1
-// and 2 issue the MMAs, warps 4-11 are two softmax warpgroups that take alternate
-// steps, one thread per TMEM lane.  A step's S and dP live in one of two 128-column
-// TMEM stages; P (bf16) is written over S and dS over dP.  S and dP are handed over
+// softmax threads, since a half's first step may not be the tile's.
+//
+// Roles (12 warps): warp 0 loads the tiles with TMA, warps 1 and 2 issue the MMAs,
+// warp 3 reads the next tile's plan and stores the results, warps 4-11 are two
+// softmax warpgroups that take alternate steps, one thread per TMEM lane.
+//
+// What bounds a step (D = 128, both halves): dq_kernel's MMAs read A from TMEM and
+// take 768 clocks, the step 950 (waits around the softmax); dkv_kernel's S and dP
+// read both operands from shared memory, 48 clocks an MMA instead of 32, and a
+// step's MMAs take 1,280, the step 1,290.  Around a tile's steps dq_kernel spends
+// some 3 us and dkv_kernel 4.5 (first loads, last products, way out).  N = 8192,
+// H = 56, 20% of the blocks: tensor pipe active 78% and 73% of the time.  Long calls
+// are at the power limit (N = 32768: 1.65 GHz), where the energy of a step counts.
+//
+// A step's S and dP live in one of two 128-column TMEM stages; P (bf16) is written over S and dS over dP.  S and dP are handed over
 // apart: S(t+2) is issued as soon as S(t) is read (dq) or dV has P(t) queued (dkv),
 // so a group starts its next exponentials while dS(t)'s products and dP(t+2) run.
 // An MMA that overwrites P or dS is issued by the warp that issued the one that
 // reads it, and the pipe keeps their order.  Two issuing warps, because the waits
 // between two batches cost the issuer 150 to 400 clocks, which the pipe's short
-// queue does not cover: while one warp waits the other's MMAs run.  Every wait is bounded; on expiry the kernel raises
-// SOL_ERR_TIMEOUT, drains what it issued and frees TMEM.
+// queue does not cover: while one warp waits the other's MMAs run.  Every wait is
+// bounded; on expiry the kernel raises SOL_ERR_TIMEOUT, drains what it issued and
+// frees TMEM.
 constexpr int kThreads = 384;            // 4 control warps + 2 softmax warpgroups
 constexpr unsigned kSms = 148;
 // A persistent CTA takes its next tile when this many steps of the present one are
 // left to load: early enough for its plan, late enough that a CTA in a long tile
-// does not hold a tile that another could run.
+// does not hold a tile that another could run (N = 38247, H = 7, prefix 2407: 5.32 ms
+// with 12 or 24, 5.35 with 4 or with a whole tile).
 constexpr int kAhead = 12;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -363,7 +376,7 @@ __device__ __forceinline__ void store_rows(const CUtensorMap* m, const uint8_t* 
 // first S and dP are computed while dQ is brought out; only dQ's accumulator is
 // waited for.  Steps, slots and barrier phases count on through the tiles.  (A CTA
 // per tile spent 12,000 clocks around its steps: launch, plan, loads, the first
-// products and the way out.)
+// products and the way out; now about 6,000.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo, const __grid_constant__ CUtensorMap mdq,
@@ -791,7 +804,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
 // The keys' pass (and, kCent, the centroids'), persistent like the queries': a tile
 // is 128 key rows (128 centroids and one range of the query blocks), its K and V
 // stay in shared memory, and the ring's slots carry the steps' Q and dO and then
-// dK and dV (fp32 gk and gv) on their way out.  The next tile's K and V are loaded
+// dV and dK (fp32 gv and gk) on their way out, each stored as it is ready.  The next tile's K and V are loaded
 // as soon as this tile's products have read theirs.
 template <int D, bool kCent>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1296,7 +1309,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
 // Per key block: the anchor's weights over its rows again, the rows' coefficients
 // (dk_t += alpha_t gk_j + beta_t a, dv_t += gamma_t gv_j) and the block's part of
 // the anchor's gradient.  One CTA a block, its K rows held in registers (K read
-// once, in mode 2 V too); HBM-bound.
+// once, in mode 2 V too).  N = 8192, H = 56, mode 2: 92 us, 3.2 TB/s (five or six
+// CTAs an SM instead of four, by fewer registers or with the rows in shared memory,
+// are no faster).
 template <int D>
 __global__ void __launch_bounds__(256, 4) pool_bwd_kernel(const BwdArgs a) {
   constexpr int LPR = D / 8, G = 256 / LPR, R = 64 / G;   // rows a lane group holds
