@@ -763,7 +763,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
       fence_after();
       const int row = 64 * in.i0 + r;
       const bool anch = a.da && (row >= a.prefix || a.prefix == a.N);
-      if (a.da && k == 0) griddep_wait();   // launched early: the anchor's gradient has to be there from here on
+      if (a.da && k == 0) griddep_wait();   // launched early: the anchor's gradient (and the pass in front) has to be complete
       const float4* da = reinterpret_cast<const float4*>(a.da + (int64_t)in.bh * D);
 #pragma unroll 1
       for (int c = g; c < D / 16; c += 2) {
@@ -1510,9 +1510,10 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   // Every launch but the first may overlap the one before it.  Who waits for what:
   // the plans need nothing of stat_kernel; tplan_kernel waits for the plans, the
   // centroids' pass for both; behind that pass nothing starts before it has these.
-  // Then dQ's pass waits only for the anchor's gradient (modes 1, 2), at a tile's end,
-  // and the keys' pass for the centroids' sums, at a tile's end.  Each kernel waits
-  // for the one before it before it is complete, so the chain ends in order.
+  // Then the keys' pass waits only for the centroids' sums and the rows' coefficients,
+  // and dQ's pass for the anchor's gradient (modes 1, 2), at their first tile's end.
+  // Each kernel waits for the one before it before it is complete, so the chain
+  // ends in order.
   // The keys' plan and the pooling start early only where the pooling's CTAs, one a
   // key block, are resident at once (four an SM): queued behind the pass in front
   // they lose more than a launch's latency (modes 1, 2; N = 1000, B = 2, H = 3: 48 us
@@ -1535,9 +1536,10 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
       if ((e = launch_kernel(anchor_bwd_kernel<D>, bh, 1024, 0, st, true, a)) != cudaSuccess) return e;
     }
   }
-  e = launch_kernel(dq_kernel<D>, std::min(tiles, kSms), kThreads, dq_smem<D>(), st, a.centroids != 0, oq, odo, mdq, mk, mv, mkb, mvb, a);
+  // (the keys' pass, the longer one, first: N = 1000, B = 2, H = 3, mode 2: 41 us, 44 the other way round)
+  e = launch_kernel(dkv_kernel<D, false>, std::min(tiles, kSms), kThreads, dkv_smem<D>(), st, a.centroids != 0, mq, mdo, ok, ov, mdk, mdv, a);
   if (e != cudaSuccess) return e;
-  return launch_kernel(dkv_kernel<D, false>, std::min(tiles, kSms), kThreads, dkv_smem<D>(), st, true, mq, mdo, ok, ov, mdk, mdv, a);
+  return launch_kernel(dq_kernel<D>, std::min(tiles, kSms), kThreads, dq_smem<D>(), st, true, oq, odo, mdq, mk, mv, mkb, mvb, a);
 }
 
 }  // namespace
