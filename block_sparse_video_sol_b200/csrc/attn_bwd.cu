@@ -285,7 +285,7 @@ struct KvBars {
   uint64_t s_full[2], dp_full[2];   // a step's S / dP are in TMEM
   uint64_t p_full[2], ds_full[2];   // P is in S's place / dS is in dP's place
   uint64_t acc_full[2], acc_clear[2];   // dK / dV are complete; read and zeroed for the next tile
-  uint64_t gb_full, out_full[2];    // group 0's offset sums are there; dK / dV are in their ring slots, to be stored
+  uint64_t gb_full[2], out_full[2]; // group 0's offset sums of a tile are there; dK / dV are in their ring slots, to be stored
   uint64_t mma_done;                // the issuers' last commits, at the end
 };
 struct KvExtra {
@@ -349,6 +349,11 @@ __device__ __forceinline__ uint64_t kmaj(uint64_t base, int kk, int chunk) {
   return base + (uint64_t)(((kk >> 2) * chunk + (kk & 3) * 32) >> 4);
 }
 
+// Eight values to a 32-byte aligned address.
+__device__ __forceinline__ void st_global32(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+}
 // Row r's 16 values of columns 16c .. 16c+15, as bf16, into a SW128 tile of 128 rows
 // (64-column chunks), the layout of the tile stores.
 template <int D>
@@ -804,15 +809,15 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
 // The keys' pass (and, kCent, the centroids'), persistent like the queries': a tile
 // is 128 key rows (128 centroids and one range of the query blocks), its K and V
 // stay in shared memory, and the ring's slots carry the steps' Q and dO and then
-// dV and dK (fp32 gv and gk) on their way out, each stored as it is ready.  The next tile's K and V are loaded
+// dV and dK on their way out, each stored as it is ready.  The next tile's K and V are loaded
 // as soon as this tile's products have read theirs.
 template <int D, bool kCent>
 __global__ void __launch_bounds__(kThreads, 1)
 dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdo,
            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-           const __grid_constant__ CUtensorMap mgk, const __grid_constant__ CUtensorMap mgv, const BwdArgs a) {
+           const __grid_constant__ CUtensorMap mdk, const __grid_constant__ CUtensorMap mdv, const BwdArgs a) {
   using C = Cfg<D>;
-  constexpr int S = C::kStages, kOut = kCent ? 4 : 2;   // ring slots; those that carry a tile's results
+  constexpr int S = C::kStages, kOut = kCent ? 0 : 2;   // ring slots; those that carry a tile's results
   extern __shared__ uint8_t smem_raw[];
   uint8_t* own = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = own + 2 * C::kOTile;
@@ -835,8 +840,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       mbar_init(&bar.acc_full[s], 1); mbar_init(&bar.acc_clear[s], 128);
     }
     for (int s = 0; s < S; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
-    mbar_init(&bar.gb_full, 128);
-    for (int s = 0; s < 2; ++s) mbar_init(&bar.out_full[s], 4);
+    for (int s = 0; s < 2; ++s) { mbar_init(&bar.gb_full[s], 128); mbar_init(&bar.out_full[s], 4); }
     mbar_init(&bar.plan_go, 1);
     mbar_init(&bar.mma_done, 2);
     x.abort_flag = 0;
@@ -1077,40 +1081,30 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (in.tile < 0) break;
       if (!wait_w(&bar.plan_go, k) || (k >= 1 && !wait_w(&bar.plan_empty[(k + 1) & 1], ((k + 1) >> 1) - 1))) break;
       plan(k + 1);
-      pos.skip(in.n);
-      // dV, then dK, each as it is ready; its slots are free (two arrivals each) once the stores have read them
-      const int row0 = 128 * in.tk, h = in.h, b = in.b, plane = in.split * bhs + in.bh;
-      RingPos<S> q = pos;
-      bool ok = true;
-      for (int o = 1; o >= 0 && (ok = wait_w(&bar.out_full[o], k)); --o) {
+      if (!kCent) {
+        pos.skip(in.n);
+        // dV, then dK, each as it is ready; its slot is free (two arrivals) once the store has read it
+        const int row0 = 128 * in.tk, h = in.h, b = in.b;
+        RingPos<S> q = pos;
+        bool ok = true;
+        for (int o = 1; o >= 0 && (ok = wait_w(&bar.out_full[o], k)); --o) {
+          if (lane == 0) store_rows(o ? &mdv : &mdk, ring + q.s * C::kOTile, row0, h, b);
+          q.next();
+        }
+        if (!ok) break;
         if (lane == 0) {
-          if (kCent) {
-            for (int c = 0; c < D / 32; ++c) {
-              const int at = c * C::kOChunk;
-              RingPos<S> w = q;
-              w.skip(at / C::kOTile);
-              tma_store_3d(o ? &mgv : &mgk, 32 * c, row0, plane, ring + w.s * C::kOTile + at % C::kOTile);
-            }
-            tma_store_commit();
-          } else {
-            store_rows(o ? &mgv : &mgk, ring + q.s * C::kOTile, row0, h, b);
+          for (int o = 0; o < kOut; ++o) {
+            if (o == 0) tma_store_wait<1>();
+            else tma_store_wait<0>();
+            RingPos<S> w = pos;
+            w.skip(o);
+            mbar_arrive(&bar.empty[w.s]);
+            mbar_arrive(&bar.empty[w.s]);
           }
         }
-        q.skip(kOut / 2);
+        pos.skip(kOut);
+        __syncwarp();
       }
-      if (!ok) break;
-      if (lane == 0) {
-        for (int o = 0; o < kOut; ++o) {
-          if (o == 0) tma_store_wait<1>();
-          if (o == kOut / 2) tma_store_wait<0>();
-          RingPos<S> w = pos;
-          w.skip(o);
-          mbar_arrive(&bar.empty[w.s]);
-          mbar_arrive(&bar.empty[w.s]);
-        }
-      }
-      pos.skip(kOut);
-      __syncwarp();
       plan_cent(k + 1);
     }
     if (lane == 0) tma_store_wait<0>();
@@ -1220,7 +1214,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       if (!ok) break;
       pos.skip(T);
       base += T;
-      // the tile's dk (gk) / dv (gv) into its ring slots, from where the planning warp stores it
+      // the tile's dk / dv into its ring slot, from where the planning warp stores it (gk / gv: to memory)
       if (!(ok = wait_w(&bar.acc_full[g], k) && wait_w(&bar.plan_cent[k & 1], k >> 1))) break;
       fence_after();
       RingPos<S> out = pos;
@@ -1232,27 +1226,28 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         gbs += odd;
         if (g == 0) {
           x.gb[k & 1][r] = gbs;
-          mbar_arrive(&bar.gb_full);
+          mbar_arrive(&bar.gb_full[k & 1]);
         } else {
-          if (!(ok = wait_w(&bar.gb_full, k))) break;
+          if (!(ok = wait_w(&bar.gb_full[k & 1], k >> 1))) break;
           if (j < a.nb) a.gb_[((int64_t)in.split * bhs + bh) * a.nb + j] = x.gb[k & 1][r] + gbs;
         }
+        // Straight to memory: a row's 32 columns are a line.  (Through ring slots and TMA stores
+        // the next tile's first steps waited for these 128 KB, 12,000 clocks from tile to
+        // tile; N = 32768, H = 56: 845 us against 800.)
+        float* row = (g ? a.gv : a.gk) + (((int64_t)in.split * bhs + bh) * a.nb + j) * D;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {   // fp32 rows: 32-column chunks of 128 bytes, SW128
-          const int at = c * C::kOChunk;
-          RingPos<S> q = out;
-          q.skip(at / C::kOTile);
-          if (!(ok = wait_w(&bar.full[q.s], q.ph))) break;
-          uint8_t* row = ring + q.s * C::kOTile + at % C::kOTile + r * 128;
+        for (int c = 0; c < D / 32; ++c) {
           float v[32];
           tmem_ld32(acc + 32 * c, v);
           tmem_wait_ld();
           clear(c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<float4*>(row + ((e ^ (r & 7)) << 4)) = make_float4(sc * v[4 * e], sc * v[4 * e + 1], sc * v[4 * e + 2], sc * v[4 * e + 3]);
+          for (int e = 0; e < 32; ++e) v[e] *= sc;
+          if (j < a.nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st_global32(row + 32 * c + 8 * e, v + 8 * e);
+          }
         }
-        if (!ok) break;
       } else {
         if (!(ok = wait_w(&bar.full[out.s], out.ph))) break;
         // the row's share of its centroid's gradient, and of the anchor's
@@ -1288,11 +1283,14 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         }
       }
       tmem_wait_st();
-      fence_async();
+      if (!kCent) fence_async();
       fence_before();
       mbar_arrive(&bar.acc_clear[g]);
       __syncwarp();
-      if (lane == 0) { mbar_arrive(&bar.out_full[g]); mbar_arrive(&bar.plan_empty[k & 1]); }
+      if (lane == 0) {
+        if (!kCent) mbar_arrive(&bar.out_full[g]);
+        mbar_arrive(&bar.plan_empty[k & 1]);
+      }
     }
   }
   fence_before();
@@ -1484,17 +1482,11 @@ bool map_cent(CUtensorMap* m, const __nv_bfloat16* p, const BwdArgs& a, int D, i
   const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)D / 64, 1};
   return make_map(m, p, 4, dims, str, box, kSw128);
 }
-bool map_part(CUtensorMap* m, const float* p, const BwdArgs& a, int D) {
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.nb, (cuuint64_t)a.splits * a.B * a.H};
-  const cuuint64_t str[2] = {(cuuint64_t)D * 4, (cuuint64_t)a.nb * D * 4};
-  const cuuint32_t box[3] = {32, 128, 1};
-  return make_map(m, p, 3, dims, str, box, kSw128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
-}
 
 template <int D>
 cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   // 64-row boxes where a tile is streamed, 128-row ones (`o`) where it is owned or a result
-  CUtensorMap mq, mk, mv, mdo, mkb, mvb, oq, ok, ov, odo, okb, ovb, mdq, mdk, mdv, mgk, mgv;
+  CUtensorMap mq, mk, mv, mdo, mkb, mvb, oq, ok, ov, odo, okb, ovb, mdq, mdk, mdv;
   auto in = [&](CUtensorMap* m, CUtensorMap* o, const __nv_bfloat16* p, int64_t sb, int64_t sn, int64_t sh) {
     return map_rows(m, p, a, D, sb, sn, sh, 64) && map_rows(o, p, a, D, sb, sn, sh, 128);
   };
@@ -1502,8 +1494,7 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   if (!in(&mq, &oq, a.q, a.sb, a.sn, a.sh) || !in(&mk, &ok, a.k, a.sb, a.sn, a.sh) || !in(&mv, &ov, a.v, a.sb, a.sn, a.sh) ||
       !in(&mdo, &odo, a.d_o, a.ob, a.on, a.oh) || !out(&mdq, a.dq) || !out(&mdk, a.dk) || !out(&mdv, a.dv) ||
       !map_cent(&mkb, a.kbar16, a, D, 64) || !map_cent(&mvb, a.vbar16, a, D, 64) ||
-      (a.centroids && (!map_cent(&okb, a.kbar16, a, D, 128) || !map_cent(&ovb, a.vbar16, a, D, 128) ||
-                       !map_part(&mgk, a.gk, a, D) || !map_part(&mgv, a.gv, a, D))))
+      (a.centroids && (!map_cent(&okb, a.kbar16, a, D, 128) || !map_cent(&ovb, a.vbar16, a, D, 128))))
     return cudaErrorInvalidValue;
   cudaError_t e = prepare<D>();
   if (e != cudaSuccess) return e;
@@ -1529,7 +1520,7 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   if ((e = launch_kernel(tplan_kernel, dim3(bh, a.mask_words), kTWarps * 32, 0, st, few, a)) != cudaSuccess) return e;
   if (a.centroids) {
     const unsigned n = std::min(bh * ((a.nb + 127) / 128) * a.splits, kSms);
-    e = launch_kernel(dkv_kernel<D, true>, n, kThreads, dkv_smem<D>(), st, true, mq, mdo, okb, ovb, mgk, mgv, a);
+    e = launch_kernel(dkv_kernel<D, true>, n, kThreads, dkv_smem<D>(), st, true, mq, mdo, okb, ovb, mdk, mdv, a);
     if (e != cudaSuccess) return e;
     if (a.mode) {
       if ((e = launch_kernel(pool_bwd_kernel<D>, dim3(bh, a.nb), 256, 0, st, few, a)) != cudaSuccess) return e;
