@@ -1505,11 +1505,11 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
   // and dQ's pass for the anchor's gradient (modes 1, 2), at their first tile's end.
   // Each kernel waits for the one before it before it is complete, so the chain
   // ends in order.
-  // The keys' plan and the pooling start early only where the pooling's CTAs, one a
-  // key block, are resident at once (four an SM): queued behind the pass in front
-  // they lose more than a launch's latency (modes 1, 2; N = 1000, B = 2, H = 3: 48 us
-  // early, 52 not; N = 8192, H = 56, 20% of the blocks: 2045 early, 1980 not).
-  const bool few = (unsigned)(a.B * a.H) * a.nb <= 4 * kSms;
+  // The keys' plan and the pooling start early only with few key blocks, a CTA of
+  // the pooling each: more of them, waiting, keep the passes off the SMs (modes 1, 2;
+  // 96 blocks, N = 1000: 41 us early, 47 not; 512, N = 4096: 133 early, 130 not; 7,168,
+  // N = 8192: 1,935 early, 1,905 not).
+  const bool few = (unsigned)(a.B * a.H) * a.nb <= 2 * kSms;
   e = launch_kernel(stat_kernel<D>, (unsigned)(a.B * a.nb) * (64 / kStatRows) * ((a.H + kStatHeads - 1) / kStatHeads), 256, 0, st, false, a);
   if (e != cudaSuccess) return e;
   AttnArgs pa{};
