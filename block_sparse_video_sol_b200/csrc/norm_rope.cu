@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdMost) norm_rope_bwd_kernel(co
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
         sx += __shfl_xor_sync(0xffffffffu, sx, o);
       }
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
+      // (past the last head: zeros, whose r without an eps would be infinite and make dw NaN)
+      const float r = live ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
       const float q = -r * r * sx * (1.f / D);
       const uint64_t r2 = f2pack(r, r), q2 = f2pack(q, q);
 #pragma unroll

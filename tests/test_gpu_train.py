@@ -737,3 +737,33 @@ def test_empty_norm_has_zero_weight_gradients(sol):
     w = torch.ones(128, device="cuda", requires_grad=True)
     sum(t.sum() for t in sol.qk_norm_rope(x, x, w, w)).backward()
     assert (w.grad == 0).all() and x.grad.shape == x.shape
+
+
+def norm_rope_bwd(sol, q, k, dqo, dko, w, cos=None, sin=None, eps=1e-6, interleaved=False):
+    """dq, dk and the two weight gradients of one call, every output NaN before it."""
+    B, N, H, D = q.shape
+    p = sol.make_params(B, N, H, D)
+    nr = sol.make_norm_rope(*w, cos, sin, eps, interleaved=interleaved)
+    dq, dk = (torch.full_like(q, float("nan")) for _ in range(2))
+    dw = [torch.full((D,), float("nan"), device="cuda") for _ in range(2)]
+    ws = torch.full((sol.sol_qk_norm_rope_bwd_workspace_bytes(p),), 255, dtype=torch.uint8, device="cuda")
+    sol.sol_qk_norm_rope_bwd(p, nr, q, k, dqo, dko, dq, dk, *dw, ws)
+    torch.cuda.synchronize()
+    return dq, dk, *dw
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", [1, 3, 9, 17])
+@pytest.mark.parametrize("inter", [False, True])
+def test_norm_rope_backward_without_eps(sol, D, H, inter):
+    """eps = 0 where the heads do not fill a warp's last unit: the lanes past the last head add nothing to the
+    weights' gradients."""
+    q, k, w, cos, sin, dqo, dko = rope_inputs(2, 37, H, D, 32, torch.float32, 0, 40 + H)
+    dq, dk, *dw = norm_rope_bwd(sol, q, k, dqo, dko, w, cos, sin, 0.0, inter)
+    c, s = f64(cos)[None], f64(sin)[None]
+    for x, wt, dz, dx, g in ((q, w[0], dqo, dq, dw[0]), (k, w[1], dko, dk, dw[1])):
+        ex, ew, mag = train_ref.norm_rope_backward(f64(x), f64(wt), c, s, 0.0, inter, f64(dz))
+        r = 1 / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True))
+        big = np.sqrt((f64(dz) ** 2).sum(-1, keepdims=True)) * f64(wt).max() * r * (1 + np.abs(f64(x)) * r)
+        assert (np.abs(f64(dx) - ex) <= U * np.abs(ex) + 2.0 ** -18 * big + 1e-30).all()
+        assert (np.abs(g.cpu().numpy() - ew) <= 2.0 ** -24 * 600 * mag + 1e-30).all()
