@@ -471,8 +471,44 @@ def backward_reblocked(p: sol_params, rb: ReblockBuffers, d_o: torch.Tensor, g: 
 
 def _like_output(d_o: torch.Tensor) -> torch.Tensor:
     """An incoming gradient as the kernels read it: bf16, contiguous, 16-byte aligned."""
-    d_o = d_o.to(torch.bfloat16).contiguous()
-    return d_o if d_o.data_ptr() % 16 == 0 else d_o.clone()
+    return _dense(d_o.to(torch.bfloat16))
+
+
+def _save(ctx, *tensors):
+    ctx.save_for_backward(*tensors)
+    ctx.kinds = [None if t is None else (t.dtype, t.shape, t.device) for t in tensors]
+
+
+def _saved(ctx):
+    """The saved tensors.  Hooks (offloading, recomputation) may give them back at other addresses and with
+    other strides, but the kernels take nothing else of another kind."""
+    tensors = ctx.saved_tensors
+    for t, kind in zip(tensors, ctx.kinds):
+        if kind is not None and (t.dtype, t.shape, t.device) != kind:
+            raise ValueError(f"a saved tensor came back as {t.dtype} {tuple(t.shape)} on {t.device}, "
+                             f"saved as {kind[0]} {tuple(kind[1])} on {kind[2]}")
+    return tensors
+
+
+def _dense(t: torch.Tensor, align: int = 16) -> torch.Tensor:
+    """The tensor contiguous and at an aligned address: itself, or a copy."""
+    t = t.contiguous()
+    return t if t.data_ptr() % align == 0 else t.clone()
+
+
+def _alike(tensors):
+    """The tensors with one set of strides that the kernels take: as they are, or dense copies."""
+    st = tensors[0].stride()
+    if st[-1] == 1 and not any(s % 8 for s in st[:-1]) and all(t.stride() == st and t.data_ptr() % 16 == 0 for t in tensors):
+        return tensors
+    return [t.clone(memory_format=torch.contiguous_format) for t in tensors]
+
+
+def _with_strides(p: sol_params, q: torch.Tensor) -> sol_params:
+    """p for inputs laid out as q."""
+    r = sol_params.from_buffer_copy(p)
+    r.in_stride_b, r.in_stride_n, r.in_stride_h = q.stride()[:3]
+    return r
 
 
 class _Attention(torch.autograd.Function):
@@ -482,16 +518,18 @@ class _Attention(torch.autograd.Function):
             buf = alloc_buffers(p, q.device, with_lse=True)
             forward(p, q, k, v, buf)
         ctx.p = p
-        ctx.save_for_backward(q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
+        _save(ctx, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
         return buf.o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_o):
-        q, k, v, ws, row_ptr, col_idx, o, lse = ctx.saved_tensors
+        q, k, v, ws, *rest = _saved(ctx)   # rest: lists, o, lse
         with torch.cuda.device(q.device):
-            g = alloc_grads(ctx.p, q.device)
-            sol_attn_bwd(ctx.p, q, k, v, ws, row_ptr, col_idx, o, lse, _like_output(d_o), g.dq, g.dk, g.dv, g.ws,
+            q, k, v = _alike((q, k, v))
+            p = _with_strides(ctx.p, q)
+            g = alloc_grads(p, q.device)
+            sol_attn_bwd(p, q, k, v, _dense(ws, 256), *map(_dense, rest), _like_output(d_o), g.dq, g.dk, g.dv, g.ws,
                          g.strides)
         return g.dq, g.dk, g.dv, None
 
@@ -530,15 +568,16 @@ class _QKNormRope(torch.autograd.Function):
         with torch.cuda.device(q.device):
             qo, ko = (torch.empty((B, N, H, D), dtype=q.dtype, device=q.device) for _ in range(2))
             sol_qk_norm_rope(ctx.p, ctx.nr, q, k, qo, ko)
-        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin)   # version checks; ctx.nr holds their addresses
+        _save(ctx, q, k, q_weight, k_weight, cos, sin)   # version checks; ctx.nr holds their addresses
         return qo, ko
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dqo, dko):
-        q, k = ctx.saved_tensors[:2]
-        p = ctx.p
+        q, k = _saved(ctx)[:2]
         with torch.cuda.device(q.device):
+            q, k = _alike((q, k))
+            p = _with_strides(ctx.p, q)
             dq, dk = (torch.empty((p.B, p.N, p.H, p.D), dtype=q.dtype, device=q.device) for _ in range(2))
             dw = [torch.zeros(p.D, device=q.device) if t is not None and ctx.needs_input_grad[2 + i] else None
                   for i, t in enumerate(ctx.wdtype)]

@@ -767,3 +767,36 @@ def test_norm_rope_backward_without_eps(sol, D, H, inter):
         big = np.sqrt((f64(dz) ** 2).sum(-1, keepdims=True)) * f64(wt).max() * r * (1 + np.abs(f64(x)) * r)
         assert (np.abs(f64(dx) - ex) <= U * np.abs(ex) + 2.0 ** -18 * big + 1e-30).all()
         assert (np.abs(g.cpu().numpy() - ew) <= 2.0 ** -24 * 600 * mag + 1e-30).all()
+
+
+def grads_of(sol, qkv, w, cos, sin, do, **kw):
+    """Gradients of one layer's step with leaves of its own."""
+    leaves = [t.detach().clone().requires_grad_() for t in (qkv, *w)]
+    _, _, o = layer(sol, leaves[0], leaves[1:], cos, sin, **kw)
+    o.backward(do)
+    return [t.grad for t in leaves]
+
+
+@pytest.mark.parametrize("mode", [0, 2])
+def test_saved_tensor_hooks_change_nothing(sol, mode):
+    """A step whose saved tensors are kept elsewhere, dense, and come back at other addresses: the fused
+    projection's views among them.  Bit for bit the plain step's gradients."""
+    B, N, H, D = 2, 300, 2, 64
+    q, k, w, cos, sin, do, _ = rope_inputs(B, N, H, D, 64, torch.float32, 0, 11)
+    qkv = torch.stack((q, k, torch.randn_like(q)), 2)
+    kw = dict(tau=0.4, log_mass_bias=mode)
+    want = grads_of(sol, qkv, w, cos, sin, do, **kw)
+    for hooks in (torch.autograd.graph.save_on_cpu(),
+                  torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: t.clone()),
+                  torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(memory_format=torch.contiguous_format), lambda t: t)):
+        with hooks:
+            got = grads_of(sol, qkv, w, cos, sin, do, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # recomputed in the backward pass
+    from torch.utils.checkpoint import checkpoint
+    leaves = [t.detach().clone().requires_grad_() for t in (qkv, *w)]
+    step = lambda x, wq, wk: sol.differentiable_attention(*sol.qk_norm_rope(*x.unbind(2)[:2], wq, wk, cos, sin),
+                                                          x.unbind(2)[2].contiguous(), **kw)
+    checkpoint(step, *leaves, use_reentrant=False).backward(do)
+    sol.sol_last_device_status()
+    assert all(torch.equal(a, t.grad) for a, t in zip(want, leaves))

@@ -191,3 +191,73 @@ def test_empty_call_without_weight_gradients_enqueues_nothing(sol):
     p = sol.make_params(1, 0, 4, 128)
     over = dict.fromkeys(("q", "k", "dqo", "dko", "dq", "dk", "dqw", "dkw", "ws"))
     assert _bwd_nr(sol, p, _nr(sol), **over) == sol.SOL_OK
+
+
+# ---- autograd functions: what the kernels are given in the backward pass -------------------------------
+def _host_autograd(sol, monkeypatch):
+    """The autograd functions on host tensors, the library's calls replaced by recorders that read what the
+    kernels would read: every (b, n, h, d) through the strides of the sol_params, inside the tensor."""
+    import contextlib
+    seen = {}
+
+    def rows(p, x):
+        st = (p.in_stride_b, p.in_stride_n, p.in_stride_h, 1)
+        last = sum((n - 1) * s for n, s in zip((p.B, p.N, p.H, p.D), st))
+        assert x.storage_offset() + last < x.untyped_storage().nbytes() // x.element_size(), "read out of range"
+        return x.as_strided((p.B, p.N, p.H, p.D), st).clone()
+
+    def attn_bwd(p, q, k, v, ws, row_ptr, col_idx, o, lse, d_o, dq, dk, dv, bws, gs):
+        seen.update(qkv=[rows(p, x) for x in (q, k, v)], o=o, ws=ws, lse=lse)
+        for t in (dq, dk, dv):
+            t.zero_()
+
+    def norm_bwd(p, nr, q, k, dqo, dko, dq, dk, dqw, dkw, ws, grad_strides):
+        seen.update(qk=[rows(p, x) for x in (q, k)], nr=nr, grad_strides=grad_strides)
+        for t in (dq, dk, dqw, dkw):
+            if t is not None:
+                t.zero_()
+
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(sol, "forward", lambda p, q, k, v, buf: [t.zero_() for t in (buf.o, buf.lse, buf.ws, buf.row_ptr, buf.col_idx)])
+    monkeypatch.setattr(sol, "sol_qk_norm_rope", lambda p, nr, q, k, qo, ko: (qo.zero_(), ko.zero_()))
+    monkeypatch.setattr(sol, "sol_attn_bwd", attn_bwd)
+    monkeypatch.setattr(sol, "sol_qk_norm_rope_bwd", norm_bwd)
+    return seen
+
+
+HOOKS = [(lambda t: t, lambda t: t),                                          # none
+         (lambda t: t.clone(memory_format=torch.contiguous_format), lambda t: t),   # dense copies, as offloading makes
+         (lambda t: t, lambda t: t if t.dim() < 4 else t.transpose(1, 2).contiguous().transpose(1, 2))]
+
+
+@pytest.mark.parametrize("hooks", HOOKS)
+def test_backward_reads_the_saved_tensors_as_they_come_back(sol, monkeypatch, hooks):
+    """Views of a fused projection, saved through hooks that give them back with other strides."""
+    seen = _host_autograd(sol, monkeypatch)
+    B, N, H, D = 2, 100, 3, 64
+    qkv = torch.randn(B, N, 3, H, D).bfloat16().requires_grad_()
+    q, k, v = qkv.unbind(2)
+    p = sol.make_params(B, N, H, D, in_strides=q.stride()[:3])
+    with torch.autograd.graph.saved_tensors_hooks(*hooks):
+        o = sol._Attention.apply(q, k, v, p)
+    o.sum().backward()
+    assert all(torch.equal(a, b) for a, b in zip(seen["qkv"], (q, k, v)))
+    assert seen["o"].is_contiguous() and seen["lse"].is_contiguous() and seen["ws"].is_contiguous()
+    with torch.autograd.graph.saved_tensors_hooks(*hooks):
+        qo, ko = sol._QKNormRope.apply(q, k, None, None, None, None, 1e-6, False)
+    (qo.sum() + ko.sum()).backward()
+    assert all(torch.equal(a, b) for a, b in zip(seen["qk"], (q, k)))
+
+
+def test_saved_tensors_of_another_kind_are_refused(sol, monkeypatch):
+    """Hooks that give back another type, shape or device: an error, not a read through a wrong address."""
+    _host_autograd(sol, monkeypatch)
+    x = torch.randn(1, 10, 1, 64).bfloat16().requires_grad_()
+    p = sol.make_params(1, 10, 1, 64)
+    for unpack in (lambda t: t.float(), lambda t: t[:, :5] if t.dim() == 4 else t, lambda t: t.to("meta")):
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: t, unpack):
+            o = sol._Attention.apply(x, x, x, p)
+            qo, _ = sol._QKNormRope.apply(x, x, None, None, None, None, 1e-6, False)
+        for t in (o, qo):
+            with pytest.raises(ValueError, match="saved"):
+                t.sum().backward()
