@@ -253,7 +253,8 @@ def sol_attn_bwd(p: sol_params, q, k, v, ws: torch.Tensor, row_ptr: torch.Tensor
 def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
                    cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, eps: float = 1e-6,
                    rot_dim: Optional[int] = None, interleaved: bool = False) -> sol_norm_rope:
-    """Fill a sol_norm_rope (it keeps the tensors alive).
+    """Fill a sol_norm_rope (it keeps the tensors alive, and holds their addresses of now: fill another
+    one when a tensor's storage has moved).
 
     The weights are [D], both fp32 or both bf16 (None: ones).  cos and sin are fp32
     [N, rot_dim/2] or [B, N, rot_dim/2] with equal strides and contiguous rows; without them
@@ -497,9 +498,9 @@ def _dense(t: torch.Tensor, align: int = 16) -> torch.Tensor:
 
 
 def _alike(tensors):
-    """The tensors with one set of strides that the kernels take: as they are, or dense copies."""
-    st = tensors[0].stride()
-    if st[-1] == 1 and not any(s % 8 for s in st[:-1]) and all(t.stride() == st and t.data_ptr() % 16 == 0 for t in tensors):
+    """The tensors with one set of strides that the kernels take (16-byte rows): as they are, or dense copies."""
+    st, unit = tensors[0].stride(), 16 // tensors[0].element_size()
+    if st[-1] == 1 and not any(s % unit for s in st[:-1]) and all(t.stride() == st and t.data_ptr() % 16 == 0 for t in tensors):
         return tensors
     return [t.clone(memory_format=torch.contiguous_format) for t in tensors]
 
@@ -563,28 +564,33 @@ class _QKNormRope(torch.autograd.Function):
     def forward(ctx, q, k, q_weight, k_weight, cos, sin, eps, interleaved):
         B, N, H, D = q.shape
         ctx.p = make_params(B, N, H, D, in_strides=q.stride()[:3])
-        ctx.nr = make_norm_rope(q_weight, k_weight, cos, sin, eps, interleaved=interleaved)
-        ctx.wdtype = [None if w is None else w.dtype for w in (q_weight, k_weight)]
+        ctx.eps, ctx.interleaved = eps, interleaved
+        nr = make_norm_rope(q_weight, k_weight, cos, sin, eps, interleaved=interleaved)
         with torch.cuda.device(q.device):
             qo, ko = (torch.empty((B, N, H, D), dtype=q.dtype, device=q.device) for _ in range(2))
-            sol_qk_norm_rope(ctx.p, ctx.nr, q, k, qo, ko)
-        _save(ctx, q, k, q_weight, k_weight, cos, sin)   # version checks; ctx.nr holds their addresses
+            sol_qk_norm_rope(ctx.p, nr, q, k, qo, ko)
+        _save(ctx, q, k, q_weight, k_weight, cos, sin)
         return qo, ko
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dqo, dko):
-        q, k = _saved(ctx)[:2]
+        q, k, *w, cos, sin = _saved(ctx)
         with torch.cuda.device(q.device):
             q, k = _alike((q, k))
+            if cos is not None:
+                cos, sin = _alike((cos, sin))
+            # addresses of now: a trainer may release the weights' storage after the forward and renew it here
+            nr = make_norm_rope(*(None if t is None else _dense(t) for t in w), cos, sin, ctx.eps,
+                                interleaved=ctx.interleaved)
             p = _with_strides(ctx.p, q)
             dq, dk = (torch.empty((p.B, p.N, p.H, p.D), dtype=q.dtype, device=q.device) for _ in range(2))
             dw = [torch.zeros(p.D, device=q.device) if t is not None and ctx.needs_input_grad[2 + i] else None
-                  for i, t in enumerate(ctx.wdtype)]
+                  for i, t in enumerate(w)]
             ws = torch.empty(max(1, sol_qk_norm_rope_bwd_workspace_bytes(p)), dtype=torch.uint8, device=q.device)
-            sol_qk_norm_rope_bwd(p, ctx.nr, q, k, _like_output(dqo), _like_output(dko), dq, dk, *dw, ws,
+            sol_qk_norm_rope_bwd(p, nr, q, k, _like_output(dqo), _like_output(dko), dq, dk, *dw, ws,
                                  grad_strides=(p.N * p.H * p.D, p.H * p.D, p.D))
-        dw = [None if g is None else g.to(t) for g, t in zip(dw, ctx.wdtype)]
+        dw = [None if g is None else g.to(t.dtype) for g, t in zip(dw, w)]
         return dq, dk, *dw, None, None, None, None
 
 

@@ -800,3 +800,34 @@ def test_saved_tensor_hooks_change_nothing(sol, mode):
     checkpoint(step, *leaves, use_reentrant=False).backward(do)
     sol.sol_last_device_status()
     assert all(torch.equal(a, t.grad) for a, t in zip(want, leaves))
+
+
+@pytest.mark.parametrize("weights", [torch.float32, torch.bfloat16])
+def test_weights_renewed_between_the_passes(sol, weights):
+    """The weights' storage is released after the forward, its memory overwritten by others, and a new one
+    filled before the backward pass, as a trainer with sharded weights does."""
+    B, N, H, D = 1, 90, 3, 128
+    q, k, w, cos, sin, dqo, dko = rope_inputs(B, N, H, D, 64, weights, 0, 21)
+    x = torch.stack((q, k), 2).requires_grad_()
+    w = [t.requires_grad_() for t in w]
+
+    def step(between):
+        x.grad = w[0].grad = w[1].grad = None
+        out = sol.qk_norm_rope(*x.unbind(2), *w, cos, sin)
+        between()
+        torch.autograd.backward(out, (dqo, dko))
+        return [t.grad.clone() for t in (x, *w)]
+
+    def renew():
+        torch.cuda.synchronize()
+        kept = [t.detach().clone() for t in w]
+        for t in w:
+            t.untyped_storage().resize_(0)
+        other.extend(torch.full((D,), 7.0, dtype=weights, device="cuda") for _ in range(16))
+        for t, c in zip(w, kept):
+            t.untyped_storage().resize_(D * t.element_size())
+            t.data.copy_(c)
+
+    other = []
+    want, got = step(lambda: None), step(renew)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

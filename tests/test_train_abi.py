@@ -261,3 +261,42 @@ def test_saved_tensors_of_another_kind_are_refused(sol, monkeypatch):
         for t in (o, qo):
             with pytest.raises(ValueError, match="saved"):
                 t.sum().backward()
+
+
+def test_backward_takes_weights_and_tables_from_the_saved_tensors(sol, monkeypatch):
+    """Weights whose storage is released after the forward and renewed before the backward pass, and weights and
+    tables that hooks give back at other addresses: the call has the addresses of what is there now."""
+    seen = _host_autograd(sol, monkeypatch)
+    B, N, H, D = 1, 10, 2, 64
+    x = torch.randn(B, N, H, D).bfloat16().requires_grad_()
+    w = [torch.randn(D, requires_grad=True) for _ in range(2)]
+    cos, sin = torch.randn(N, 16), torch.randn(N, 16)
+    args = lambda: (x, x, *w, cos, sin, 1e-5, True)
+    addresses = lambda: [seen["nr"].q_weight, seen["nr"].k_weight, seen["nr"].cos, seen["nr"].sin]
+
+    qo, ko = sol._QKNormRope.apply(*args())
+    kept, other = [t.detach().clone() for t in w], []
+    for t, c in zip(w, kept):
+        t.untyped_storage().resize_(0)
+        other.append(torch.empty(D))          # takes the place
+        t.untyped_storage().resize_(4 * D)
+        t.data.copy_(c)
+    (qo.sum() + ko.sum()).backward()
+    assert addresses() == [t.data_ptr() for t in (*w, cos, sin)]
+    assert abs(seen["nr"].eps - 1e-5) < 1e-11 and seen["nr"].interleaved == 1 and seen["nr"].rot_dim == 32
+
+    # (a copy one element into its storage: made aligned; tables whose rows are not contiguous: made dense)
+    def unpack(t):
+        if t.dtype != torch.float32:
+            return t
+        if t.dim() == 2:
+            return t.t().contiguous().t()
+        return torch.cat((torch.zeros(1), t.detach()))[1:]
+
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, unpack):
+        qo, ko = sol._QKNormRope.apply(*args())
+    (qo.sum() + ko.sum()).backward()
+    nr = seen["nr"]
+    assert not set(addresses()) & {t.data_ptr() for t in (*w, cos, sin)}
+    assert all(a % 16 == 0 for a in addresses()) and nr.table_stride_n == 16
+    assert all(torch.equal(a, b) for a, b in zip(nr.tensors, (*w, cos, sin)))
