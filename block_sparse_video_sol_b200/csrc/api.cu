@@ -631,7 +631,8 @@ sol_status sol_debug_drop_arrive(int32_t step) {
   sol_status s = check_arch();
   if (s != SOL_OK) return s;
   if (step < -1) return fail(SOL_ERR_INVALID_ARG, "sol_debug_drop_arrive: step %d < -1", (int)step);
-  const cudaError_t e = sol::set_drop_p_arrive(step);
+  cudaError_t e = sol::set_drop_p_arrive(step);
+  if (e == cudaSuccess) e = sol::set_drop_ds_arrive(step);
   if (e != cudaSuccess) return cuda_fail(e, "sol_debug_drop_arrive");
   return SOL_OK;
 #else

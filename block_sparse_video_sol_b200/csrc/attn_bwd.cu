@@ -32,6 +32,15 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Fault-test build: the "dS ready" arrive of a tile's step g_drop_ds_arrive is withheld, so
+// that the issuing warp's bounded wait for dS expires (sol_debug_drop_arrive).
+#ifdef SOL_FAULT_TEST
+__device__ int g_drop_ds_arrive = -1;
+__device__ __forceinline__ bool withheld(int step) { return step == g_drop_ds_arrive; }
+#else
+__device__ __forceinline__ bool withheld(int) { return false; }
+#endif
+
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -751,7 +760,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtens
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ds_full[g]);
+        if (lane == 0 && !withheld(u - base)) mbar_arrive(&bar.ds_full[g]);
       }
       if (!ok) break;
       base += T;
@@ -861,7 +870,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
       RingPos<S> pos;
-      int slots = 0, owns = 0;
+      int slots = 0, owns[2] = {0, 0};   // armed loads: ring slots; K's, V's
       bool ok = true;
       auto slot = [&]() { return ok = ok && wait(&bar.empty[pos.s], pos.ph ^ 1u); };
       auto next = [&]() { pos.next(); ++slots; };
@@ -870,14 +879,15 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         const KvTile& in = x.info[k & 1];
         if (in.tile < 0) break;
         const int tk = in.tk, h = in.h, b = in.b, T = in.n;
+#pragma unroll
         for (int o = 0; o < 2; ++o) {   // K, V, once the previous tile's products have read theirs
           if (k > 0 && !(ok = ok && wait(&bar.own_free[o], k - 1))) break;
           mbar_expect_tx(&bar.own_full[o], C::kOTile);
           if (kCent) tma_load_4d(own + o * C::kOTile, o ? &mv : &mk, 0, 128 * tk, 0, in.bh, &bar.own_full[o]);
           else load_rows(own + o * C::kOTile, o ? &mv : &mk, 128 * tk, h, b, &bar.own_full[o]);
+          ++owns[o];   // (counted apart: V's wait may give up with K's load on its way)
         }
         if (!ok) break;
-        ++owns;
         const int go = max(0, T - kAhead);
         if (T == 0) mbar_arrive(&bar.plan_go);
         for (int t = 0; t < T && slot(); ++t, next()) {   // Q and dO, -lse and -delta of their rows
@@ -894,10 +904,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
       }
       // every armed load has landed before the CTA may exit
       for (int i = max(0, slots - S); i < slots; ++i) drain_bar(&bar.full[i % S], (i / S) & 1, a.status);
-      if (owns) {
-        drain_bar(&bar.own_full[0], (owns - 1) & 1, a.status);
-        drain_bar(&bar.own_full[1], (owns - 1) & 1, a.status);
-      }
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        if (owns[o]) drain_bar(&bar.own_full[o], (owns[o] - 1) & 1, a.status);
     }
   } else if (warp == 1 || warp == 2) {
     // ---------------------------------------------------------------- products
@@ -1209,7 +1218,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUten
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ds_full[g]);
+        if (lane == 0 && !withheld(u - base)) mbar_arrive(&bar.ds_full[g]);
       }
       if (!ok) break;
       pos.skip(T);
@@ -1542,6 +1551,12 @@ cudaError_t launch(const BwdArgs& a, cudaStream_t st) {
 // is what a tile's way in and out costs (N = 4096, H = 56: 43 us against 61 with
 // eight), and at most eight ranges for the partial sums' memory.
 int attn_bwd_splits(int nb) { return nb <= 32 ? (nb + 3) / 4 : std::min(8, (nb + 15) / 16); }
+
+#ifdef SOL_FAULT_TEST
+cudaError_t set_drop_ds_arrive(int step) {
+  return cudaMemcpyToSymbol(g_drop_ds_arrive, &step, sizeof(int));
+}
+#endif
 
 cudaError_t launch_attn_bwd(const BwdArgs& a, int D, cudaStream_t st) {
   return D == 128 ? launch<128>(a, st) : launch<64>(a, st);

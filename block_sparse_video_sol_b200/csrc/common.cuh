@@ -164,6 +164,7 @@ cudaError_t launch_rows(const int32_t* perm, const __nv_bfloat16* src, __nv_bflo
 cudaError_t launch_plan(const AttnArgs& a, cudaStream_t st, bool early = false);
 #ifdef SOL_FAULT_TEST
 cudaError_t set_drop_p_arrive(int step);   // fault-test build only
+cudaError_t set_drop_ds_arrive(int step);
 #endif
 
 // ---- attention backward (sol_attn_bwd) ---------------------------------------------------------

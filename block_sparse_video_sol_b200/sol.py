@@ -327,7 +327,8 @@ def sol_last_device_status(stream=None):
 
 def sol_debug_drop_arrive(step: int):
     """Fault-test library only: withhold the attention's "P ready" arrive of S
-    tile `step` in every CTA (-1: none), so that its bounded wait expires."""
+    tile `step` in every CTA (-1: none), so that its bounded wait expires; in
+    the gradient's passes the "dS ready" arrive of that step."""
     _check(lib.sol_debug_drop_arrive(step), "sol_debug_drop_arrive")
 
 

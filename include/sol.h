@@ -386,7 +386,9 @@ sol_status sol_qk_norm_rope_bwd(const sol_params* p, const sol_norm_rope* nr, co
  * step `step` (0-based S tile; -1 restores normal operation), so the MMA
  * warp's bounded wait expires.  That launch then stops issuing, drains its
  * copies and MMAs, frees its tensor memory, writes no output and leaves
- * SOL_ERR_TIMEOUT in the device status word; the context stays usable.
+ * SOL_ERR_TIMEOUT in the device status word; the context stays usable.  The
+ * passes of sol_attn_bwd withhold the "dS ready" arrive of the same step of
+ * every tile and end in the same way (their gradients are then incomplete).
  * Synchronous (a symbol copy), not for use while kernels run.  Returns
  * SOL_ERR_INVALID_ARG for step < -1; the product library returns
  * SOL_ERR_UNSUPPORTED and changes nothing. */
