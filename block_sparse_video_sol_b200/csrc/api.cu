@@ -475,7 +475,7 @@ sol_status check_norm_rope(const sol_params* p, const sol_norm_rope* nr, const c
   if (nr->interleaved != 0 && nr->interleaved != 1) return fail(SOL_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1", name);
   if (!aligned16(nr->q_weight) || !aligned16(nr->k_weight)) return fail(SOL_ERR_INVALID_ARG, "%s: weights not 16-byte aligned", name);
   if (nr->rot_dim > 0) {
-    if (!nr->cos || !nr->sin) return fail(SOL_ERR_INVALID_ARG, "%s: NULL table", name);
+    if (!empty(p) && (!nr->cos || !nr->sin)) return fail(SOL_ERR_INVALID_ARG, "%s: NULL table", name);
     if (!aligned16(nr->cos) || !aligned16(nr->sin)) return fail(SOL_ERR_INVALID_ARG, "%s: tables not 16-byte aligned", name);
     if (nr->table_stride_b < 0 || nr->table_stride_n < 0 || (nr->table_stride_b & 3) || (nr->table_stride_n & 3))
       return fail(SOL_ERR_INVALID_ARG, "%s: table strides must be >= 0 and multiples of 4 elements", name);

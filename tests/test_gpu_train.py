@@ -831,3 +831,14 @@ def test_weights_renewed_between_the_passes(sol, weights):
     other = []
     want, got = step(lambda: None), step(renew)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_empty_sequence_through_autograd_with_tables(sol):
+    x = torch.empty(2, 0, 4, 128, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    w = torch.ones(128, device="cuda", requires_grad=True)
+    t = torch.empty(0, 64, device="cuda")
+    q, k = sol.qk_norm_rope(x, x, w, w, t, t)
+    o = sol.differentiable_attention(q, k, x)
+    assert o.shape == x.shape
+    o.sum().backward()
+    assert (w.grad == 0).all() and x.grad.shape == x.shape

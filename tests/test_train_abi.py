@@ -300,3 +300,16 @@ def test_backward_takes_weights_and_tables_from_the_saved_tensors(sol, monkeypat
     assert not set(addresses()) & {t.data_ptr() for t in (*w, cos, sin)}
     assert all(a % 16 == 0 for a in addresses()) and nr.table_stride_n == 16
     assert all(torch.equal(a, b) for a, b in zip(nr.tensors, (*w, cos, sin)))
+
+
+def test_empty_calls_take_empty_tables(sol):
+    """Tables of no positions (or of no batch entries) have no address: with B or N = 0 that is a valid call."""
+    for B, N, tables in ((2, 0, torch.zeros(0, 32)), (2, 0, torch.zeros(2, 0, 32)), (0, 5, torch.zeros(0, 5, 32))):
+        p = sol.make_params(B, N, 4, 128)
+        nr = sol.make_norm_rope(None, None, tables, tables.clone())
+        assert nr.rot_dim == 64 and not nr.cos
+        assert _fwd_nr(sol, p, nr, None, None, None, None) == sol.SOL_OK, _text(sol)
+        over = dict.fromkeys(("q", "k", "dqo", "dko", "dq", "dk", "dqw", "dkw", "ws"))
+        assert _bwd_nr(sol, p, nr, **over) == sol.SOL_OK, _text(sol)
+    full = sol.make_params(2, 5, 4, 128)
+    assert _fwd_nr(sol, full, nr) == sol.SOL_ERR_INVALID_ARG and "NULL table" in _text(sol)
