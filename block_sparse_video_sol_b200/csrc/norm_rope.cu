@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdMost) norm_rope_bwd_kernel(co
       }
       // (past the last head: zeros, whose r without an eps would be infinite and make dw NaN)
       const float r = live ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
-      const float q = -r * r * sx * (1.f / D);
+      const float q = -r * (r * sx) * (1.f / D);   // (r sx is about |u|; r r overflows below |x| = 5e-20)
       const uint64_t r2 = f2pack(r, r), q2 = f2pack(q, q);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -842,3 +842,26 @@ def test_empty_sequence_through_autograd_with_tables(sol):
     assert o.shape == x.shape
     o.sum().backward()
     assert (w.grad == 0).all() and x.grad.shape == x.shape
+
+
+@pytest.mark.parametrize("size", [4e-20, 1e-12, 1e12, 1e17])
+def test_norm_rope_of_tiny_and_huge_rows(sol, size):
+    """Rows of one size far from 1 without an eps: r^2 alone would overflow (4e-20: r = 2.5e19).  The squares of the
+    smallest are subnormal, off by half of 2^-149 each: 2e-7 of r, inside the bound's 2^-18."""
+    B, N, H, D = 1, 33, 3, 128
+    q, k, w, cos, sin, dqo, dko = rope_inputs(B, N, H, D, 64, torch.float32, 0, 31)
+    q, k = ((t.float() / t.float().square().mean(-1, keepdim=True).sqrt() * size).bfloat16() for t in (q, k))
+    p = sol.make_params(B, N, H, D)
+    nr = sol.make_norm_rope(*w, cos, sin, 0.0)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    sol.sol_qk_norm_rope(p, nr, q, k, qo, ko)
+    dq, dk, *dw = norm_rope_bwd(sol, q, k, dqo, dko, w, cos, sin, 0.0)
+    c, s = f64(cos)[None], f64(sin)[None]
+    for x, wt, y, dz, dx, g in ((q, w[0], qo, dqo, dq, dw[0]), (k, w[1], ko, dko, dk, dw[1])):
+        r = 1 / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True))
+        want = train_ref.norm_rope(f64(x), f64(wt), c, s, 0.0, False)
+        assert (np.abs(f64(y) - want) <= U * np.abs(want) + 2.0 ** -17 * f64(wt).max() * np.abs(f64(x) * r).max(-1, keepdims=True)).all()
+        ex, ew, mag = train_ref.norm_rope_backward(f64(x), f64(wt), c, s, 0.0, False, f64(dz))
+        big = np.sqrt((f64(dz) ** 2).sum(-1, keepdims=True)) * f64(wt).max() * r * (1 + np.abs(f64(x)) * r)
+        assert (np.abs(f64(dx) - ex) <= U * np.abs(ex) + 2.0 ** -18 * big).all()
+        assert (np.abs(g.cpu().numpy() - ew) <= 2.0 ** -24 * 600 * mag).all()
