@@ -453,16 +453,25 @@ def backward(p: sol_params, q, k, v, buf: Buffers, d_o: torch.Tensor, g: GradBuf
     return g
 
 
+def _with_strides(p: sol_params, q: torch.Tensor) -> sol_params:
+    """p for inputs laid out as q."""
+    r = sol_params.from_buffer_copy(p)
+    r.in_stride_b, r.in_stride_n, r.in_stride_h = q.stride()[:3]
+    return r
+
+
 def backward_reblocked(p: sol_params, rb: ReblockBuffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
-    """Gradient of ``forward_reblocked`` (rb as it left it, with an lse) for d_o laid out as p's
-    in_strides: gather d_o into the partition's order, the backward pass there, scatter the three
-    gradients back into ``g`` (g.ws from alloc_grads of the same shape)."""
+    """Gradient of ``forward_reblocked`` (rb as it left it, with an lse) for d_o, a bf16 tensor
+    [B, N, H, D] of any strides the kernels take: gather it into the partition's order, the backward
+    pass there, scatter the three gradients back into ``g`` (g.ws from alloc_grads of the same shape)."""
     if rb.buf.lse is None:
         raise ValueError("the backward pass needs the forward's lse (alloc_reblock(with_lse=True))")
+    if d_o.dtype != torch.bfloat16 or d_o.shape != rb.qp.transpose(1, 2).shape or d_o.stride(3) != 1:
+        raise ValueError("d_o must be bf16 [B, N, H, D] with contiguous head dim")
     hm = (p.H * p.N * p.D, p.D, p.N * p.D)
     with torch.cuda.stream(stream):   # memory of the stream that uses it
         dop, dqp, dkp, dvp = (torch.empty_like(rb.qp) for _ in range(4))
-    sol_gather_rows(p, rb.perm, d_o, dop, stream)
+    sol_gather_rows(_with_strides(p, d_o), rb.perm, d_o, dop, stream)
     sol_attn_bwd(rb.hm, rb.qp, rb.kp, rb.vp, rb.buf.ws, rb.buf.row_ptr, rb.buf.col_idx, rb.buf.o, rb.buf.lse, dop, dqp,
                  dkp, dvp, g.ws, hm, stream)
     to = make_params(p.B, p.N, p.H, p.D, prefix_len=p.prefix_len, out_strides=g.strides)
@@ -504,13 +513,6 @@ def _alike(tensors):
     if st[-1] == 1 and not any(s % unit for s in st[:-1]) and all(t.stride() == st and t.data_ptr() % 16 == 0 for t in tensors):
         return tensors
     return [t.clone(memory_format=torch.contiguous_format) for t in tensors]
-
-
-def _with_strides(p: sol_params, q: torch.Tensor) -> sol_params:
-    """p for inputs laid out as q."""
-    r = sol_params.from_buffer_copy(p)
-    r.in_stride_b, r.in_stride_n, r.in_stride_h = q.stride()[:3]
-    return r
 
 
 class _Attention(torch.autograd.Function):

@@ -865,3 +865,22 @@ def test_norm_rope_of_tiny_and_huge_rows(sol, size):
         big = np.sqrt((f64(dz) ** 2).sum(-1, keepdims=True)) * f64(wt).max() * r * (1 + np.abs(f64(x)) * r)
         assert (np.abs(f64(dx) - ex) <= U * np.abs(ex) + 2.0 ** -18 * big).all()
         assert (np.abs(g.cpu().numpy() - ew) <= 2.0 ** -24 * 600 * mag).all()
+
+
+def test_reblocked_backward_of_fused_views(sol):
+    """q, k, v as views of the fused projection and a dense d_o: the bits of the dense call."""
+    w = synth.tiny()
+    q, k, v = (parity.to_dev(x) for x in synth.generate(w))
+    do = torch.randn_like(q)
+    kw = dict(tau=w.tau, log_mass_bias=2)
+    fused = torch.stack((q, k, v), 2).unbind(2)
+    out = []
+    for x, d in (((q, k, v), do), (fused, do), (fused, torch.stack((do, q), 2)[:, :, 0])):
+        p = sol.make_params(w.B, w.N, w.H, w.D, in_strides=x[0].stride()[:3], **kw)
+        rb = sol.alloc_reblock(p, "cuda", with_lse=True)
+        sol.forward_reblocked(p, *x, torch.empty_like(q), rb)
+        g = sol.backward_reblocked(p, rb, d, sol.alloc_grads(p, "cuda"))
+        sol.sol_last_device_status()
+        out.append((g.dq, g.dk, g.dv))
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0], other))

@@ -313,3 +313,32 @@ def test_empty_calls_take_empty_tables(sol):
         assert _bwd_nr(sol, p, nr, **over) == sol.SOL_OK, _text(sol)
     full = sol.make_params(2, 5, 4, 128)
     assert _fwd_nr(sol, full, nr) == sol.SOL_ERR_INVALID_ARG and "NULL table" in _text(sol)
+
+
+@pytest.mark.parametrize("layout", ["dense", "fused", "expanded", "head-major"])
+def test_reblocked_gradient_reads_d_o_where_it_lies(sol, monkeypatch, layout):
+    """q, k, v are views of a fused projection; the output's gradient has a layout of its own."""
+    B, N, H, D = 1, 100, 2, 64
+    fused = torch.randn(B, N, 3, H, D).bfloat16()
+    q = fused.unbind(2)[0]
+    p = sol.make_params(B, N, H, D, in_strides=q.stride()[:3])
+    d_o = {"dense": torch.randn(B, N, H, D).bfloat16(), "fused": torch.randn(B, N, 3, H, D).bfloat16()[:, :, 1],
+           "expanded": torch.randn(D).bfloat16().expand(B, N, H, D),
+           "head-major": torch.randn(B, H, N, D).bfloat16().transpose(1, 2)}[layout]
+    seen = []
+
+    def gather(gp, perm, x, xp, stream=None):
+        st = (gp.in_stride_b, gp.in_stride_n, gp.in_stride_h, 1)
+        last = x.storage_offset() + sum((n - 1) * s for n, s in zip((B, N, H, D), st))
+        assert last < x.untyped_storage().nbytes() // 2, "read out of range"
+        seen.append(x.as_strided((B, N, H, D), st))
+
+    monkeypatch.setattr(sol, "sol_gather_rows", gather)
+    monkeypatch.setattr(sol, "sol_attn_bwd", lambda *a, **k: None)
+    monkeypatch.setattr(sol, "sol_scatter_rows", lambda *a, **k: None)
+    rb = sol.alloc_reblock(p, "cpu", with_lse=True)
+    sol.backward_reblocked(p, rb, d_o, sol.alloc_grads(p, "cpu"))
+    assert torch.equal(seen[0], d_o)
+    for bad in (d_o.float(), d_o[:, :50], torch.randn(B, N, H, 2 * D).bfloat16()[..., ::2]):
+        with pytest.raises(ValueError, match="d_o"):
+            sol.backward_reblocked(p, rb, bad, sol.alloc_grads(p, "cpu"))
