@@ -448,6 +448,10 @@ def backward(p: sol_params, q, k, v, buf: Buffers, d_o: torch.Tensor, g: GradBuf
     """Enqueue the gradient of ``forward`` (buf as it left it, with an lse) for d_o (p's out_strides)."""
     if buf.lse is None:
         raise ValueError("the backward pass needs the forward's lse (alloc_buffers(with_lse=True))")
+    want = (p.out_stride_b, p.out_stride_n, p.out_stride_h, 1)
+    if d_o.dtype != torch.bfloat16 or d_o.shape != (p.B, p.N, p.H, p.D) or any(
+            n > 1 and a != b for n, a, b in zip(d_o.shape, d_o.stride(), want)):
+        raise ValueError("d_o must be bf16 [B, N, H, D] with p's out_strides (as buf.o)")
     sol_attn_bwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse, d_o, g.dq, g.dk, g.dv, g.ws, g.strides,
                  stream)
     return g

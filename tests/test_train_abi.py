@@ -342,3 +342,24 @@ def test_reblocked_gradient_reads_d_o_where_it_lies(sol, monkeypatch, layout):
     for bad in (d_o.float(), d_o[:, :50], torch.randn(B, N, H, 2 * D).bfloat16()[..., ::2]):
         with pytest.raises(ValueError, match="d_o"):
             sol.backward_reblocked(p, rb, bad, sol.alloc_grads(p, "cpu"))
+
+
+def test_backward_refuses_a_gradient_that_is_not_laid_out_as_the_output(sol, monkeypatch):
+    """o and d_o share p's out_strides: an expanded, transposed or fp32 d_o would be read past its end."""
+    B, N, H, D = 1, 64, 2, 64
+    x = torch.randn(B, N, H, D).bfloat16()
+    p = sol.make_params(B, N, H, D)
+    buf, g, calls = sol.alloc_buffers(p, "cpu", with_lse=True), sol.alloc_grads(p, "cpu"), []
+    monkeypatch.setattr(sol, "sol_attn_bwd", lambda *a, **k: calls.append(a))
+    for bad in (torch.ones(()).bfloat16().expand(B, N, H, D), x.transpose(1, 2), x.float(), x[:, :5],
+                torch.zeros(B, H, N, D).bfloat16().transpose(1, 2)):
+        with pytest.raises(ValueError, match="d_o"):
+            sol.backward(p, x, x, x, buf, bad, g)
+    assert not calls
+    sol.backward(p, x, x, x, buf, x, g)
+    fused = torch.randn(B, N, 2, H, D).bfloat16()[:, :, 1]
+    p2 = sol.make_params(B, N, H, D, out_strides=fused.stride()[:3])
+    sol.backward(p2, x, x, x, buf, fused, g)
+    one = sol.make_params(1, 1, H, D)   # dims of one: any stride
+    sol.backward(one, x[:, :1], x[:, :1], x[:, :1], buf, x[:, 3:4], g)
+    assert len(calls) == 3
