@@ -31,9 +31,11 @@ def rows_of(N: int, nb: int, j: int):
     return np.arange(64 * j, min(N, 64 * (j + 1)))
 
 
-def attention_backward(Q, K, V, dO, O, lse, sel, kc, vc, off, prefix=0, mode=0, centroids=True, scale=None):
+def attention_backward(Q, K, V, dO, O, lse, sel, kc, vc, off, prefix=0, mode=0, centroids=True, scale=None,
+                       tap=lambda name, x: x):
     """Gradients (and bounds) of one (b, h): Q, K, V, dO, O [N, D]; lse [N]; sel [nb, nb];
-    kc, vc [nb, D] and off [nb] the centroid operands as the attention read them."""
+    kc, vc [nb, D] and off [nb] the centroid operands as the attention read them.  ``tap`` sees a few
+    intermediate values by name and returns what is used instead: tests plant mistakes with it."""
     N, D = Q.shape
     s = 1.0 / math.sqrt(D) if scale is None else scale
     nb = sel.shape[0]
@@ -70,7 +72,7 @@ def attention_backward(Q, K, V, dO, O, lse, sel, kc, vc, off, prefix=0, mode=0, 
         dq, bq = dq + g, bq + b
         gk, egk = prod(s * dsc.T, s * dscm.T, Q)
         gv, egv = prod(pc.T, 0 * pc.T, dO)
-        gb = dsc.sum(0)
+        gb = tap("gb terms", dsc).sum(0)
         egb = e1 * np.abs(dsc).sum(0) + e2 * dscm.sum(0)
         lo = prefix if prefix < N else 0
         a = Q[lo:].mean(0)
@@ -92,14 +94,15 @@ def attention_backward(Q, K, V, dO, O, lse, sel, kc, vc, off, prefix=0, mode=0, 
                 al = np.full(n, 1.0 / n)
                 beta = s * gb[j] * (w - 1.0 / n) if mode == 1 else np.zeros(n)
                 eb = s * (egb[j] + e1 * abs(gb[j])) * np.abs(w - 1.0 / n) + e1 * s * abs(gb[j]) * (w + 1.0 / n) if mode == 1 else np.zeros(n)
-            dk[r] += al[:, None] * gk[j] + beta[:, None] * a
+            dk[r] += al[:, None] * gk[j] + tap("beta of dk", beta)[:, None] * a
             bk[r] += al[:, None] * (egk[j] + e1 * np.abs(gk[j])) + (eb + e1 * np.abs(beta))[:, None] * np.abs(a)
             dv[r] += al[:, None] * gv[j]
             bv[r] += al[:, None] * (egv[j] + e1 * np.abs(gv[j]))
             da += beta @ K[r]
             eda += (eb + e1 * np.abs(beta)) @ aK[r]
         if mode:
-            dq[lo:] += da / (N - lo)
+            at = tap("first anchor row", lo)
+            dq[at:] += tap("da", da) / (N - at)
             bq[lo:] += eda / (N - lo)
     return [(g, b + U * np.abs(g) + 1e-30) for g, b in ((dq, bq), (dk, bk), (dv, bv))]
 

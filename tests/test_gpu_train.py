@@ -14,7 +14,7 @@ import torch
 
 from block_sparse_video_sol_b200 import synth
 from oracle import sol_ref, train_ref
-from tests import parity
+from tests import anchor_cases, parity
 
 pytestmark = pytest.mark.gpu
 
@@ -884,3 +884,25 @@ def test_reblocked_backward_of_fused_views(sol):
         out.append((g.dq, g.dk, g.dv))
     for other in out[1:]:
         assert all(torch.equal(a, b) for a, b in zip(out[0], other))
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("N,D,prefix", anchor_cases.CASES)
+def test_anchor_s_terms(sol, N, D, prefix, mode):
+    """Inputs on which the anchor's terms are far above the roundings (a CPU test plants mistakes in them)."""
+    heads = [anchor_cases.inputs(N, D, prefix, seed) for seed in range(3)]
+    q, k, v, do = (torch.from_numpy(np.stack([h[i] for h in heads], 1)[None]).cuda().bfloat16() for i in range(4))
+    p = sol.make_params(1, N, 3, D, prefix_len=prefix, log_mass_bias=mode)
+    buf, g = sol.alloc_buffers(p, "cuda", with_lse=True), sol.alloc_grads(p, "cuda")
+    sol.sol_pool(p, q, k, v, buf.ws)
+    sel = torch.from_numpy(np.concatenate([h[4] for h in heads]))
+    buf.row_ptr.copy_(torch.nn.functional.pad(sel.sum(1).cumsum(0), (1, 0)))
+    entries = sel.nonzero()[:, 1].int().cuda()
+    buf.col_idx[:len(entries)] = entries
+    sol.sol_attn_fwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
+    for t in (g.dq, g.dk, g.dv):
+        t.fill_(float("nan"))
+    g.ws.fill_(255)
+    sol.backward(p, q, k, v, buf, do, g)
+    sol.sol_last_device_status()
+    check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import sol_ref, train_ref
+from tests import anchor_cases
 
 
 def _problem(N, D, prefix, seed):
@@ -114,3 +115,31 @@ def test_rotation_is_orthogonal_and_pairs_as_named():
         a, b = (2, 3) if inter else (1, 4)
         assert np.allclose(z[0, 1, 0, a] + 1j * z[0, 1, 0, b],
                            (y[0, 1, 0, a] + 1j * y[0, 1, 0, b]) * np.exp(1j * ang[0, 1, 1]))
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("N,D,prefix", anchor_cases.CASES)
+def test_bounds_catch_mistakes_in_the_anchor_s_terms(N, D, prefix, mode):
+    """On the inputs of the GPU's anchor test every one of these mistakes exceeds the bound twice over."""
+    Q, K, V, dO, sel = anchor_cases.inputs(N, D, prefix)
+    kc, vc, off = train_ref.centroid_operands(Q, K, V, prefix, mode)
+    kc, vc = sol_ref.bf16_round(kc), sol_ref.bf16_round(vc)
+    lse = _lse(Q, K, kc, off, sel, True)
+    blk, s = np.arange(N) // 64, 1.0 / math.sqrt(D)
+    p = np.exp(np.where(sel[blk][:, blk], s * Q @ K.T, -np.inf) - lse[:, None])
+    pc = np.exp(np.where(sel[blk], -np.inf, s * Q @ kc.T + off) - lse[:, None])
+    O = sol_ref.bf16_round(p @ V + pc @ vc)
+    back = lambda tap: train_ref.attention_backward(Q, K, V, dO, O, lse, sel, kc, vc, off, prefix, mode, tap=tap)
+    want = back(lambda name, x: x)
+    nb = len(sel)
+    splits = (nb + 3) // 4 if nb <= 32 else min(8, (nb + 15) // 16)   # query ranges of the centroid pass
+    first = (np.arange(N) < 64 * (nb // splits))[:, None]
+    plant = {"no da": ("da", lambda x: 0 * x), "da's sign": ("da", lambda x: -x),
+             "no gb": ("gb terms", lambda x: 0 * x), "no beta a": ("beta of dk", lambda x: 0 * x)}
+    if splits > 1:
+        plant["gb of the first range only"] = "gb terms", lambda x: np.where(first, x, 0.0)
+    if 0 < prefix < N:
+        plant["da on every row"] = "first anchor row", lambda x: 0
+    for mistake, (at, f) in plant.items():
+        got = back(lambda name, x: f(x) if name == at else x)
+        assert max((np.abs(g - w) / b).max() for (g, _), (w, b) in zip(got, want)) >= 2.0, mistake
