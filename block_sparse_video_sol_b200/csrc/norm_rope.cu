@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdMost) norm_rope_bwd_kernel(co
     for (int k = 0; k < kHeads; ++k) {
       const bool live = h0 + GPW * k < a.H;
       uint64_t f[4], z[4], zp[4], ss2 = 0ull, sx2 = 0ull;
-      uint4 u = make_uint4(0, 0, 0, 0), v = u;
+      // past the last head: a row of ones (r = 1 / sqrt(0) would be infinite) whose dz = 0 adds nothing to dw
+      uint4 u = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), v = make_uint4(0, 0, 0, 0);
       if (live) {
         u = ring[(stage * 2 * kHeads + 2 * k) * 32];
         v = ring[(stage * 2 * kHeads + 2 * k + 1) * 32];
@@ -338,9 +339,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdMost) norm_rope_bwd_kernel(co
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
         sx += __shfl_xor_sync(0xffffffffu, sx, o);
       }
-      // (past the last head: zeros, whose r without an eps would be infinite and make dw NaN)
-      const float r = live ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
-      const float q = -r * (r * sx) * (1.f / D);   // (r sx is about |u|; r r overflows below |x| = 5e-20)
+      const float r = rsqrtf(ss * (1.f / D) + a.eps);
+      const float q = r * (-1.f / D) * (r * sx);   // (r sx is about |u|; r r overflows below |x| = 5e-20)
       const uint64_t r2 = f2pack(r, r), q2 = f2pack(q, q);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
