@@ -76,17 +76,18 @@ __device__ __forceinline__ void load_weight(const NormRopeArgs& a, int t, int d0
 // What a lane (chunk c of a row, dims 8c .. 8c+7) needs to turn its dims at one
 // position: cos, the sine with the sign of the forward turn, and the lane
 // chunk that holds the partners (its own with interleaved pairs or outside
-// the turned dims, where cos = 1 and sin = 0).
+// the turned dims).  There (c, s) = (1, 0); in the backward kernel with split pairs,
+// where a dim is its own partner, halves of it, so that an infinity stays one.
 struct Turn {
   float c[8], s[8];
   int partner;
 };
-template <bool kInter>
+template <bool kInter, bool kHalves = false>
 __device__ __forceinline__ void load_turn(const NormRopeArgs& a, int b, int n, int c, Turn& t) {
   t.partner = c;
   if (8 * c >= 2 * a.half) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { t.c[i] = 1.f; t.s[i] = 0.f; }
+    for (int i = 0; i < 8; ++i) { t.c[i] = kHalves ? 0.5f : 1.f; t.s[i] = kHalves ? -0.5f : 0.f; }
     return;
   }
   const int64_t row = (int64_t)b * a.tb + (int64_t)n * a.tn;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdMost) norm_rope_bwd_kernel(co
   while (at.t == 0) {
     if (fresh) {   // uniform over the warp
       Turn tr;
-      load_turn<kInter>(a, at.b, at.n, c, tr);
+      load_turn<kInter, !kInter>(a, at.b, at.n, c, tr);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         cs[e] = f2pack(tr.c[2 * e], tr.c[2 * e + 1]);

@@ -354,7 +354,8 @@ typedef struct {
  * the pairs (a, b) of the turned dims become (a cos - b sin, b cos + a sin);
  * fp32 inside, rounded once (values past 1e18 overflow the mean square, and their
  * row becomes zeros; without an eps, rows of values below 1e-20 lose bits of it, and
- * rows of zeros become NaN).
+ * rows of zeros become NaN; a non-finite value makes NaN of its own pair, with
+ * interleaved pairs also past the turned dims).
  *   q, k     [B, N, H, D] bf16, strides p->in_stride_* (e.g. views of the fused
  *            QKV projection);  qo, ko  the same shape, strides p->out_stride_*,
  *            distinct rows.  qo = q and ko = k in place is allowed with equal

@@ -906,3 +906,33 @@ def test_anchor_s_terms(sol, N, D, prefix, mode):
     sol.backward(p, q, k, v, buf, do, g)
     sol.sol_last_device_status()
     check_grads(sol, p, buf, q, k, v, do, (g.dq, g.dk, g.dv))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("inter", [False, True])
+def test_infinite_values_outside_the_turned_dims(sol, D, inter):
+    """An infinity past the turned dims reaches the other dims through the norm alone (with interleaved pairs
+    its neighbour becomes NaN too); other rows and the other tensor keep their bits."""
+    at = 41
+    q, k, w, cos, sin, dqo, dko = rope_inputs(1, 20, 3, D, 32, torch.float32, 0, 51)
+    p = sol.make_params(1, 20, 3, D)
+    qi, zi = q.clone(), dqo.clone()
+    qi[0, 7, 1, at] = float("inf")
+    zi[0, 7, 1, at] = float("inf")
+    nr = sol.make_norm_rope(*w, cos, sin, interleaved=inter)
+    qo, ko = (torch.full_like(q, 3.0) for _ in range(2))
+    sol.sol_qk_norm_rope(p, nr, qi, k, qo, ko)
+    torch.cuda.synchronize()
+    other = torch.arange(D, device="cuda") != at
+    if inter:
+        other[at - 1] = False
+    assert torch.isnan(qo[0, 7, 1, ~other]).all() and (qo[0, 7, 1, other] == 0).all()   # x / infinity
+    dq, dk, dwq, dwk = norm_rope_bwd(sol, q, k, zi, dko, w, cos, sin, interleaved=inter)
+    clean = norm_rope_bwd(sol, q, k, dqo, dko, w, cos, sin, interleaved=inter)
+    assert not torch.isfinite(dwq[~other]).any() and torch.equal(dwq[other], clean[2][other])
+    assert torch.equal(dk, clean[1]) and torch.equal(dwk, clean[3])
+    if not inter:
+        assert torch.isinf(dwq[at]) and torch.isinf(dq[0, 7, 1, other]).all()   # each less x times the mean of u x
+    assert not torch.isfinite(dq[0, 7, 1]).any()
+    dq[0, 7, 1] = clean[0][0, 7, 1]
+    assert torch.equal(dq, clean[0])
