@@ -265,6 +265,8 @@ def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Te
         if (w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != weights[0].dtype or not w.is_contiguous()
                 or w.dim() != 1 or w.shape != weights[0].shape):
             raise ValueError("the weights must be contiguous, of one length, both fp32 or both bf16")
+    if any(t is not None and t.numel() and not t.data_ptr() for t in (q_weight, k_weight, cos, sin)):
+        raise ValueError("a weight or table has no storage")   # a NULL weight would mean ones
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     sb = sn = 0

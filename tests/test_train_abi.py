@@ -363,3 +363,15 @@ def test_backward_refuses_a_gradient_that_is_not_laid_out_as_the_output(sol, mon
     one = sol.make_params(1, 1, H, D)   # dims of one: any stride
     sol.backward(one, x[:, :1], x[:, :1], x[:, :1], buf, x[:, 3:4], g)
     assert len(calls) == 3
+
+
+def test_weights_and_tables_without_storage_are_refused(sol):
+    """A weight whose storage was released (sharded weights not gathered) has no address: NULL would mean ones."""
+    w, t = torch.ones(64), torch.zeros(10, 32)
+    empty = [x.clone() for x in (w, t)]
+    for x in empty:
+        x.untyped_storage().resize_(0)
+    for args in ((empty[0], None), (None, empty[0]), (w, w, empty[1], t), (w, w, t, empty[1])):
+        with pytest.raises(ValueError, match="storage"):
+            sol.make_norm_rope(*args)
+    assert sol.make_norm_rope(w, w, torch.zeros(0, 32), torch.zeros(0, 32)).rot_dim == 64   # no positions
