@@ -250,6 +250,19 @@ def sol_attn_bwd(p: sol_params, q, k, v, ws: torch.Tensor, row_ptr: torch.Tensor
            "sol_attn_bwd")
 
 
+def _place(nr: sol_norm_rope, q_weight, k_weight, cos, sin):
+    """The addresses of now and the tables' strides into nr, which keeps the tensors alive."""
+    nr.tensors = (q_weight, k_weight, cos, sin)
+    nr.q_weight, nr.k_weight = _ptr(q_weight), _ptr(k_weight)
+    if nr.rot_dim:
+        nr.cos, nr.sin = _ptr(cos), _ptr(sin)
+        nr.table_stride_n = cos.stride(-2) if cos.shape[-2] > 1 else 0
+        nr.table_stride_b = cos.stride(0) if cos.dim() == 3 and cos.shape[0] > 1 else 0
+    if ((q_weight is not None and not nr.q_weight) or (k_weight is not None and not nr.k_weight)
+            or (nr.rot_dim and cos.numel() and not (nr.cos and nr.sin))):
+        raise ValueError("a weight or table has no storage")   # (a NULL weight would mean ones)
+
+
 def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
                    cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, eps: float = 1e-6,
                    rot_dim: Optional[int] = None, interleaved: bool = False) -> sol_norm_rope:
@@ -265,11 +278,8 @@ def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Te
         if (w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != weights[0].dtype or not w.is_contiguous()
                 or w.dim() != 1 or w.shape != weights[0].shape):
             raise ValueError("the weights must be contiguous, of one length, both fp32 or both bf16")
-    if any(t is not None and t.numel() and not t.data_ptr() for t in (q_weight, k_weight, cos, sin)):
-        raise ValueError("a weight or table has no storage")   # a NULL weight would mean ones
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    sb = sn = 0
     if cos is None:
         if rot_dim:
             raise ValueError("rot_dim needs the cos and sin tables")
@@ -282,13 +292,9 @@ def make_norm_rope(q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Te
             raise ValueError(f"rot_dim {rot_dim} needs tables of width {rot_dim // 2}, got {cos.shape[-1]}")
         if cos.numel() and (cos.stride() != sin.stride() or cos.stride(-1) != 1):
             raise ValueError("cos and sin must have identical strides and contiguous rows")
-        if rot_dim:
-            sn = cos.stride(-2) if cos.shape[-2] > 1 else 0
-            sb = cos.stride(0) if cos.dim() == 3 and cos.shape[0] > 1 else 0
-    nr = sol_norm_rope(_ptr(q_weight), _ptr(k_weight), int(bool(weights) and weights[0].dtype == torch.bfloat16),
-                       float(eps), int(rot_dim), int(bool(interleaved)), _ptr(cos) if rot_dim else None,
-                       _ptr(sin) if rot_dim else None, sb, sn)
-    nr.tensors = (q_weight, k_weight, cos, sin)
+    nr = sol_norm_rope(weight_type=int(bool(weights) and weights[0].dtype == torch.bfloat16), eps=float(eps),
+                       rot_dim=int(rot_dim), interleaved=int(bool(interleaved)))
+    _place(nr, q_weight, k_weight, cos, sin)
     # what they cover: head dims, positions, batch entries (None: any)
     nr.covers = (weights[0].shape[0] if weights else None, cos.shape[-2] if rot_dim else None,
                  cos.shape[0] if rot_dim and cos.dim() == 3 and cos.shape[0] > 1 else None)
@@ -491,20 +497,17 @@ def _like_output(d_o: torch.Tensor) -> torch.Tensor:
     return _dense(d_o.to(torch.bfloat16))
 
 
-def _save(ctx, *tensors):
-    ctx.save_for_backward(*tensors)
-    ctx.kinds = [None if t is None else (t.dtype, t.shape, t.device) for t in tensors]
-
-
-def _saved(ctx):
-    """The saved tensors.  Hooks (offloading, recomputation) may give them back at other addresses and with
-    other strides, but the kernels take nothing else of another kind."""
-    tensors = ctx.saved_tensors
-    for t, kind in zip(tensors, ctx.kinds):
-        if kind is not None and (t.dtype, t.shape, t.device) != kind:
+def _check_saved(p: sol_params, rows, others, device):
+    """Saved tensors as their hooks (offloading, recomputation) give them back: at any address and with any
+    strides, but nothing of another kind.  rows are [B, N, H, D] bf16, others (tensor, dtype, elements)."""
+    shape = (p.B, p.N, p.H, p.D)
+    for t in rows:
+        if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device:
             raise ValueError(f"a saved tensor came back as {t.dtype} {tuple(t.shape)} on {t.device}, "
-                             f"saved as {kind[0]} {tuple(kind[1])} on {kind[2]}")
-    return tensors
+                             f"not bf16 {shape} on {device}")
+    for t, dtype, n in others:
+        if t is not None and (t.dtype is not dtype or t.numel() != n or t.device != device):
+            raise ValueError(f"a saved tensor came back as {t.numel()} {t.dtype} on {t.device}, not {n} {dtype} on {device}")
 
 
 def _dense(t: torch.Tensor, align: int = 16) -> torch.Tensor:
@@ -513,12 +516,16 @@ def _dense(t: torch.Tensor, align: int = 16) -> torch.Tensor:
     return t if t.data_ptr() % align == 0 else t.clone()
 
 
-def _alike(tensors):
-    """The tensors with one set of strides that the kernels take (16-byte rows): as they are, or dense copies."""
-    st, unit = tensors[0].stride(), 16 // tensors[0].element_size()
-    if st[-1] == 1 and not any(s % unit for s in st[:-1]) and all(t.stride() == st and t.data_ptr() % 16 == 0 for t in tensors):
-        return tensors
-    return [t.clone(memory_format=torch.contiguous_format) for t in tensors]
+def _laid_out(p: sol_params, tensors):
+    """The tensors with one set of strides that the kernels take, as they are or as dense copies, and p for
+    these strides."""
+    st = tensors[0].stride()
+    if st[3] != 1 or (st[0] | st[1] | st[2]) & 7 or any(t.stride() != st or t.data_ptr() & 15 for t in tensors):
+        tensors = [t.clone(memory_format=torch.contiguous_format) for t in tensors]
+        st = tensors[0].stride()
+    if st[:3] != (p.in_stride_b, p.in_stride_n, p.in_stride_h):
+        p = _with_strides(p, tensors[0])
+    return p, tensors
 
 
 class _Attention(torch.autograd.Function):
@@ -527,20 +534,22 @@ class _Attention(torch.autograd.Function):
         with torch.cuda.device(q.device):
             buf = alloc_buffers(p, q.device, with_lse=True)
             forward(p, q, k, v, buf)
-        ctx.p = p
-        _save(ctx, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
+        ctx.p, ctx.sizes = p, (buf.ws.numel(), buf.row_ptr.numel(), buf.col_idx.numel())
+        ctx.save_for_backward(q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse)
         return buf.o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_o):
-        q, k, v, ws, *rest = _saved(ctx)   # rest: lists, o, lse
-        with torch.cuda.device(q.device):
-            q, k, v = _alike((q, k, v))
-            p = _with_strides(ctx.p, q)
-            g = alloc_grads(p, q.device)
-            sol_attn_bwd(p, q, k, v, _dense(ws, 256), *map(_dense, rest), _like_output(d_o), g.dq, g.dk, g.dv, g.ws,
-                         g.strides)
+        q, k, v, ws, row_ptr, col_idx, o, lse = ctx.saved_tensors
+        device, n_ws, n_rows, n_cols = d_o.device, *ctx.sizes
+        _check_saved(ctx.p, (q, k, v, o), ((ws, torch.uint8, n_ws), (row_ptr, torch.int32, n_rows), (col_idx, torch.int32, n_cols),
+                                           (lse, torch.float32, ctx.p.B * ctx.p.H * ctx.p.N)), device)
+        with torch.cuda.device(device):
+            p, (q, k, v) = _laid_out(ctx.p, (q, k, v))
+            g = alloc_grads(p, device)
+            sol_attn_bwd(p, q, k, v, _dense(ws, 256), _dense(row_ptr), _dense(col_idx), _dense(o), _dense(lse),
+                         _like_output(d_o), g.dq, g.dk, g.dv, g.ws, g.strides)
         return g.dq, g.dk, g.dv, None
 
 
@@ -573,30 +582,33 @@ class _QKNormRope(torch.autograd.Function):
     def forward(ctx, q, k, q_weight, k_weight, cos, sin, eps, interleaved):
         B, N, H, D = q.shape
         ctx.p = make_params(B, N, H, D, in_strides=q.stride()[:3])
-        ctx.eps, ctx.interleaved = eps, interleaved
         nr = make_norm_rope(q_weight, k_weight, cos, sin, eps, interleaved=interleaved)
+        ctx.nr, ctx.n_table = sol_norm_rope.from_buffer_copy(nr), 0 if cos is None else cos.numel()   # (not the tensors)
         with torch.cuda.device(q.device):
             qo, ko = (torch.empty((B, N, H, D), dtype=q.dtype, device=q.device) for _ in range(2))
             sol_qk_norm_rope(ctx.p, nr, q, k, qo, ko)
-        _save(ctx, q, k, q_weight, k_weight, cos, sin)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin)
         return qo, ko
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dqo, dko):
-        q, k, *w, cos, sin = _saved(ctx)
-        with torch.cuda.device(q.device):
-            q, k = _alike((q, k))
-            if cos is not None:
-                cos, sin = _alike((cos, sin))
+        q, k, *w, cos, sin = ctx.saved_tensors
+        device, wdtype = dqo.device, torch.bfloat16 if ctx.nr.weight_type else torch.float32
+        _check_saved(ctx.p, (q, k), ((w[0], wdtype, ctx.p.D), (w[1], wdtype, ctx.p.D), (cos, torch.float32, ctx.n_table),
+                                     (sin, torch.float32, ctx.n_table)), device)
+        with torch.cuda.device(device):
+            p, (q, k) = _laid_out(ctx.p, (q, k))
+            if cos is not None and (cos.stride() != sin.stride() or cos.stride(-1) != 1 or (cos.data_ptr() | sin.data_ptr()) & 15):
+                cos, sin = (t.clone(memory_format=torch.contiguous_format) for t in (cos, sin))
             # addresses of now: a trainer may release the weights' storage after the forward and renew it here
-            nr = make_norm_rope(*(None if t is None else _dense(t) for t in w), cos, sin, ctx.eps,
-                                interleaved=ctx.interleaved)
-            p = _with_strides(ctx.p, q)
-            dq, dk = (torch.empty((p.B, p.N, p.H, p.D), dtype=q.dtype, device=q.device) for _ in range(2))
-            dw = [torch.zeros(p.D, device=q.device) if t is not None and ctx.needs_input_grad[2 + i] else None
+            nr = sol_norm_rope.from_buffer_copy(ctx.nr)
+            w = [None if t is None else _dense(t) for t in w]
+            _place(nr, *w, cos, sin)
+            dq, dk = (torch.empty((p.B, p.N, p.H, p.D), dtype=q.dtype, device=device) for _ in range(2))
+            dw = [torch.empty(p.D, device=device) if t is not None and ctx.needs_input_grad[2 + i] else None
                   for i, t in enumerate(w)]
-            ws = torch.empty(max(1, sol_qk_norm_rope_bwd_workspace_bytes(p)), dtype=torch.uint8, device=q.device)
+            ws = torch.empty(max(1, sol_qk_norm_rope_bwd_workspace_bytes(p)), dtype=torch.uint8, device=device)
             sol_qk_norm_rope_bwd(p, nr, q, k, _like_output(dqo), _like_output(dko), dq, dk, *dw, ws,
                                  grad_strides=(p.N * p.H * p.D, p.H * p.D, p.D))
         dw = [None if g is None else g.to(t.dtype) for g, t in zip(dw, w)]

@@ -375,3 +375,18 @@ def test_weights_and_tables_without_storage_are_refused(sol):
         with pytest.raises(ValueError, match="storage"):
             sol.make_norm_rope(*args)
     assert sol.make_norm_rope(w, w, torch.zeros(0, 32), torch.zeros(0, 32)).rot_dim == 64   # no positions
+
+
+def test_saved_tensors_of_another_size_are_refused(sol, monkeypatch):
+    _host_autograd(sol, monkeypatch)
+    x = torch.randn(1, 100, 1, 64).bfloat16().requires_grad_()
+    w, t = torch.randn(64, requires_grad=True), torch.randn(100, 16)
+    p = sol.make_params(1, 100, 1, 64)
+    short = lambda dims: lambda s: s[..., :1] if s.dim() == dims and s.numel() > 1 else s
+    for dims, run in ((1, lambda: sol._Attention.apply(x, x, x, p)), (3, lambda: sol._Attention.apply(x, x, x, p)),
+                      (1, lambda: sol._QKNormRope.apply(x, x, w, None, t, t, 1e-6, False)[0]),
+                      (2, lambda: sol._QKNormRope.apply(x, x, w, None, t, t, 1e-6, False)[0])):
+        with torch.autograd.graph.saved_tensors_hooks(lambda s: s, short(dims)):
+            out = run()
+        with pytest.raises(ValueError, match="saved"):
+            out.sum().backward()
