@@ -452,14 +452,21 @@ def alloc_grads(p: sol_params, device) -> GradBuffers:
     return GradBuffers(ws, dq, dk, dv, (p.N * p.H * p.D, p.H * p.D, p.D))
 
 
+def _like_out(p: sol_params, d_o: torch.Tensor, o: torch.Tensor) -> bool:
+    """Whether d_o is laid out by p's out_strides: as [B, N, H, D], as o, or dense in some other shape."""
+    dims, want = (p.B, p.N, p.H, p.D), (p.out_stride_b, p.out_stride_n, p.out_stride_h, 1)
+    if d_o.shape == dims:
+        return (d_o.stride() == want or (d_o.shape == o.shape and d_o.stride() == o.stride())
+                or not any(n > 1 and a != b for n, a, b in zip(dims, d_o.stride(), want)))
+    return d_o.is_contiguous() and d_o.numel() > sum((n - 1) * s for n, s in zip(dims, want))
+
+
 def backward(p: sol_params, q, k, v, buf: Buffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
     """Enqueue the gradient of ``forward`` (buf as it left it, with an lse) for d_o (p's out_strides)."""
     if buf.lse is None:
         raise ValueError("the backward pass needs the forward's lse (alloc_buffers(with_lse=True))")
-    want = (p.out_stride_b, p.out_stride_n, p.out_stride_h, 1)
-    if d_o.dtype != torch.bfloat16 or d_o.shape != (p.B, p.N, p.H, p.D) or any(
-            n > 1 and a != b for n, a, b in zip(d_o.shape, d_o.stride(), want)):
-        raise ValueError("d_o must be bf16 [B, N, H, D] with p's out_strides (as buf.o)")
+    if d_o.dtype != torch.bfloat16 or not _like_out(p, d_o, buf.o):
+        raise ValueError("d_o must be bf16 and laid out by p's out_strides, as buf.o")
     sol_attn_bwd(p, q, k, v, buf.ws, buf.row_ptr, buf.col_idx, buf.o, buf.lse, d_o, g.dq, g.dk, g.dv, g.ws, g.strides,
                  stream)
     return g

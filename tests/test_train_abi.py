@@ -390,3 +390,31 @@ def test_saved_tensors_of_another_size_are_refused(sol, monkeypatch):
             out = run()
         with pytest.raises(ValueError, match="saved"):
             out.sum().backward()
+
+
+def test_backward_takes_head_major_and_flat_gradients(sol, monkeypatch):
+    """Layouts that are the output's although the tensor's shape is not [B, N, H, D]."""
+    calls = []
+    monkeypatch.setattr(sol, "sol_attn_bwd", lambda *a, **k: calls.append(a))
+    for N in (64, 2):   # (N = H: the shapes are alike)
+        B, H, D = 2, 2, 64
+        p = sol.make_params(B, N, H, D)
+        hm = sol.head_major_params(p)
+        x = torch.randn(B, N, H, D).bfloat16()
+        xh = x.transpose(1, 2).contiguous()
+        buf = sol.alloc_buffers(hm, "cpu", with_lse=True, head_major_out=True)
+        g = sol.alloc_grads(p, "cpu")
+        for d_o in (xh, xh.view(-1), xh.transpose(1, 2)):
+            sol.backward(hm, xh, xh, xh, buf, d_o, g)
+        flat = sol.alloc_buffers(p, "cpu", with_lse=True)
+        for d_o in (x, x.view(B, N, H * D), x.view(-1)):
+            sol.backward(p, x, x, x, flat, d_o, g)
+        for q, b, d_o in ((p, flat, x.view(-1)[:-8]), (p, flat, x.view(B, N, H * D)[:, :, ::2])):
+            with pytest.raises(ValueError, match="d_o"):
+                sol.backward(q, x, x, x, b, d_o, g)
+    with pytest.raises(ValueError, match="d_o"):   # the output is head-major, d_o is not
+        p = sol.make_params(1, 64, 2, 64)
+        x = torch.randn(1, 64, 2, 64).bfloat16()
+        hm = sol.head_major_params(p)
+        sol.backward(hm, x, x, x, sol.alloc_buffers(hm, "cpu", with_lse=True, head_major_out=True), x, sol.alloc_grads(p, "cpu"))
+    assert len(calls) == 12
