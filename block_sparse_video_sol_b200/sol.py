@@ -458,7 +458,12 @@ def _like_out(p: sol_params, d_o: torch.Tensor, o: torch.Tensor) -> bool:
     if d_o.shape == dims:
         return (d_o.stride() == want or (d_o.shape == o.shape and d_o.stride() == o.stride())
                 or not any(n > 1 and a != b for n, a, b in zip(dims, d_o.stride(), want)))
-    return d_o.is_contiguous() and d_o.numel() > sum((n - 1) * s for n, s in zip(dims, want))
+    return _spans(p, d_o, want)
+
+
+def _spans(p: sol_params, t: torch.Tensor, strides) -> bool:
+    """Whether a dense tensor holds every element that the strides reach."""
+    return t.is_contiguous() and t.numel() > sum((n - 1) * s for n, s in zip((p.B, p.N, p.H, p.D), strides))
 
 
 def backward(p: sol_params, q, k, v, buf: Buffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
@@ -481,16 +486,18 @@ def _with_strides(p: sol_params, q: torch.Tensor) -> sol_params:
 
 def backward_reblocked(p: sol_params, rb: ReblockBuffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
     """Gradient of ``forward_reblocked`` (rb as it left it, with an lse) for d_o, a bf16 tensor
-    [B, N, H, D] of any strides the kernels take: gather it into the partition's order, the backward
-    pass there, scatter the three gradients back into ``g`` (g.ws from alloc_grads of the same shape)."""
+    [B, N, H, D] of any strides the kernels take (or a dense one of another shape, laid out as p's
+    in_strides): gather it into the partition's order, the backward pass there, scatter the three
+    gradients back into ``g`` (g.ws from alloc_grads of the same shape)."""
     if rb.buf.lse is None:
         raise ValueError("the backward pass needs the forward's lse (alloc_reblock(with_lse=True))")
-    if d_o.dtype != torch.bfloat16 or d_o.shape != rb.qp.transpose(1, 2).shape or d_o.stride(3) != 1:
+    rows = d_o.shape == (p.B, p.N, p.H, p.D) and d_o.stride(3) == 1
+    if d_o.dtype != torch.bfloat16 or (not rows and not _spans(p, d_o, (p.in_stride_b, p.in_stride_n, p.in_stride_h, 1))):
         raise ValueError("d_o must be bf16 [B, N, H, D] with contiguous head dim")
     hm = (p.H * p.N * p.D, p.D, p.N * p.D)
     with torch.cuda.stream(stream):   # memory of the stream that uses it
         dop, dqp, dkp, dvp = (torch.empty_like(rb.qp) for _ in range(4))
-    sol_gather_rows(_with_strides(p, d_o), rb.perm, d_o, dop, stream)
+    sol_gather_rows(_with_strides(p, d_o) if rows else p, rb.perm, d_o, dop, stream)
     sol_attn_bwd(rb.hm, rb.qp, rb.kp, rb.vp, rb.buf.ws, rb.buf.row_ptr, rb.buf.col_idx, rb.buf.o, rb.buf.lse, dop, dqp,
                  dkp, dvp, g.ws, hm, stream)
     to = make_params(p.B, p.N, p.H, p.D, prefix_len=p.prefix_len, out_strides=g.strides)

@@ -418,3 +418,21 @@ def test_backward_takes_head_major_and_flat_gradients(sol, monkeypatch):
         hm = sol.head_major_params(p)
         sol.backward(hm, x, x, x, sol.alloc_buffers(hm, "cpu", with_lse=True, head_major_out=True), x, sol.alloc_grads(p, "cpu"))
     assert len(calls) == 12
+
+
+def test_reblocked_gradient_takes_flat_gradients_laid_out_as_the_inputs(sol, monkeypatch):
+    B, N, H, D = 1, 100, 2, 64
+    x = torch.randn(B, N, H, D).bfloat16()
+    seen = []
+    monkeypatch.setattr(sol, "sol_gather_rows", lambda gp, perm, t, tp, stream=None: seen.append(
+        (t.data_ptr(), gp.in_stride_b, gp.in_stride_n, gp.in_stride_h)))
+    monkeypatch.setattr(sol, "sol_attn_bwd", lambda *a, **k: None)
+    monkeypatch.setattr(sol, "sol_scatter_rows", lambda *a, **k: None)
+    for p, shapes in ((sol.make_params(B, N, H, D), ((B, N, H * D), (-1,))),
+                      (sol.head_major_params(sol.make_params(B, N, H, D)), ((B, H, N, D),))):
+        rb = sol.alloc_reblock(p, "cpu", with_lse=True)
+        for shape in shapes:
+            sol.backward_reblocked(p, rb, x.view(shape), sol.alloc_grads(p, "cpu"))
+            assert seen.pop() == (x.data_ptr(), p.in_stride_b, p.in_stride_n, p.in_stride_h)
+        with pytest.raises(ValueError, match="d_o"):
+            sol.backward_reblocked(p, rb, x.view(-1)[:-8], sol.alloc_grads(p, "cpu"))
