@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(1024) dw_kernel(const NormRopeArgs a, int part
 // with 12 warps, 343 with 16, 360 with 24; backward 437 / 493 us with 12 / 16).  With
 // few heads a position's angles are most of the work and more warps win (H = 8:
 // forward 82 us with 12 warps, 66 with 24, backward 103 / 90 us with 12 / 16; the
-// two meet at 32 heads of 128 dims, four chunks).  A job is a whole position where every warp
+// two meet at 32 heads of 128 dims, four chunks; one box, the same buffers in every
+// call: buffers that change cost 10 to 15% more).  A job is a whole position where every warp
 // gets several, else a single head chunk (short calls: more warps at work).
 struct Plan {
   Grid g;
