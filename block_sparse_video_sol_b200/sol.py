@@ -452,18 +452,24 @@ def alloc_grads(p: sol_params, device) -> GradBuffers:
     return GradBuffers(ws, dq, dk, dv, (p.N * p.H * p.D, p.H * p.D, p.D))
 
 
+def _lies(dims, tensor_strides, strides) -> bool:
+    return not any(n > 1 and a != b for n, a, b in zip(dims, tensor_strides, strides))
+
+
+def _lies_by(p: sol_params, t: torch.Tensor, strides) -> bool:
+    """Whether a tensor that is not [B, N, H, D] lies as the strides say: rows of joined heads [B, N, H D],
+    or any dense one that holds every element they reach."""
+    if t.shape == (p.B, p.N, p.H * p.D):
+        return (p.H == 1 or strides[2] == p.D) and _lies(t.shape, t.stride(), (strides[0], strides[1], 1))
+    return t.is_contiguous() and t.numel() > sum((n - 1) * s for n, s in zip((p.B, p.N, p.H, p.D), strides))
+
+
 def _like_out(p: sol_params, d_o: torch.Tensor, o: torch.Tensor) -> bool:
-    """Whether d_o is laid out by p's out_strides: as [B, N, H, D], as o, or dense in some other shape."""
+    """Whether d_o is laid out by p's out_strides: as [B, N, H, D], as o, or in another shape."""
     dims, want = (p.B, p.N, p.H, p.D), (p.out_stride_b, p.out_stride_n, p.out_stride_h, 1)
     if d_o.shape == dims:
-        return (d_o.stride() == want or (d_o.shape == o.shape and d_o.stride() == o.stride())
-                or not any(n > 1 and a != b for n, a, b in zip(dims, d_o.stride(), want)))
-    return _spans(p, d_o, want)
-
-
-def _spans(p: sol_params, t: torch.Tensor, strides) -> bool:
-    """Whether a dense tensor holds every element that the strides reach."""
-    return t.is_contiguous() and t.numel() > sum((n - 1) * s for n, s in zip((p.B, p.N, p.H, p.D), strides))
+        return d_o.stride() == want or (d_o.shape == o.shape and d_o.stride() == o.stride()) or _lies(dims, d_o.stride(), want)
+    return _lies_by(p, d_o, want)
 
 
 def backward(p: sol_params, q, k, v, buf: Buffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
@@ -486,13 +492,13 @@ def _with_strides(p: sol_params, q: torch.Tensor) -> sol_params:
 
 def backward_reblocked(p: sol_params, rb: ReblockBuffers, d_o: torch.Tensor, g: GradBuffers, stream=None) -> GradBuffers:
     """Gradient of ``forward_reblocked`` (rb as it left it, with an lse) for d_o, a bf16 tensor
-    [B, N, H, D] of any strides the kernels take (or a dense one of another shape, laid out as p's
+    [B, N, H, D] of any strides the kernels take (or one of another shape, laid out as p's
     in_strides): gather it into the partition's order, the backward pass there, scatter the three
     gradients back into ``g`` (g.ws from alloc_grads of the same shape)."""
     if rb.buf.lse is None:
         raise ValueError("the backward pass needs the forward's lse (alloc_reblock(with_lse=True))")
     rows = d_o.shape == (p.B, p.N, p.H, p.D) and d_o.stride(3) == 1
-    if d_o.dtype != torch.bfloat16 or (not rows and not _spans(p, d_o, (p.in_stride_b, p.in_stride_n, p.in_stride_h, 1))):
+    if d_o.dtype != torch.bfloat16 or (not rows and not _lies_by(p, d_o, (p.in_stride_b, p.in_stride_n, p.in_stride_h, 1))):
         raise ValueError("d_o must be bf16 [B, N, H, D] with contiguous head dim")
     hm = (p.H * p.N * p.D, p.D, p.N * p.D)
     with torch.cuda.stream(stream):   # memory of the stream that uses it

@@ -436,3 +436,27 @@ def test_reblocked_gradient_takes_flat_gradients_laid_out_as_the_inputs(sol, mon
             assert seen.pop() == (x.data_ptr(), p.in_stride_b, p.in_stride_n, p.in_stride_h)
         with pytest.raises(ValueError, match="d_o"):
             sol.backward_reblocked(p, rb, x.view(-1)[:-8], sol.alloc_grads(p, "cpu"))
+
+
+def test_gradients_of_joined_heads_are_taken_where_they_lie(sol, monkeypatch):
+    """d_o as [B, N, H D], a view of something wider (the projection behind the attention takes such rows)."""
+    calls, gathers = [], []
+    monkeypatch.setattr(sol, "sol_attn_bwd", lambda *a, **k: calls.append(a))
+    monkeypatch.setattr(sol, "sol_gather_rows", lambda gp, *a: gathers.append(gp))
+    monkeypatch.setattr(sol, "sol_scatter_rows", lambda *a: None)
+    B, N, H, D = 2, 30, 2, 64
+    x = torch.randn(B, N, H, D).bfloat16()
+    wide = torch.randn(B, N, 3 * H * D).bfloat16()[:, :, H * D:2 * H * D]
+    st = (N * 3 * H * D, 3 * H * D, D)
+    p = sol.make_params(B, N, H, D, in_strides=st, out_strides=st)
+    buf, g = sol.alloc_buffers(p, "cpu", with_lse=True), sol.alloc_grads(p, "cpu")
+    sol.backward(p, x, x, x, buf, wide, g)
+    rb = sol.alloc_reblock(p, "cpu", with_lse=True)
+    sol.backward_reblocked(p, rb, wide, g)
+    assert len(calls) == 2 and gathers[0].in_stride_n == 3 * H * D
+    dense = wide.contiguous()
+    for bad_p in (p, sol.head_major_params(p)):   # rows closer together than p says; heads that are not joined
+        with pytest.raises(ValueError, match="d_o"):
+            sol.backward(bad_p, x, x, x, buf, dense, g)
+        with pytest.raises(ValueError, match="d_o"):
+            sol.backward_reblocked(bad_p, rb, dense, g)
